@@ -32,6 +32,11 @@ MOE_FLAG_DEQUANT_TO_HBM = 0x10
 MOE_FLAG_NO_ROUTER = 0x20
 MOE_FLAG_NO_EXPERTS = 0x40
 MOE_FLAG_TEST_STALL = 0x100
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_FP16 = 1
+MOE_DTYPE_FP32 = 2
+MOE_ACT_NONE = 0
+MOE_ACT_SWIGLU = 1
 
 _ERR_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED_DEVICE", 3: "TOO_LARGE", 4: "CUDA",
               5: "DEVICE_TIMEOUT", 6: "DEVICE_BOUNDS", 7: "RANGE"}
@@ -89,6 +94,26 @@ def lib() -> ctypes.CDLL:
         L.moe_route_static.argtypes = [P, I32, I32, P, P, I32, I32, P, P, P]
         L.moe_forward_routed.argtypes = [P, P, I32, P, P, P, P, P]
         L.moe_combine_rows.argtypes = [P, P, I32, P, I32, I32, P, P, P]
+        I64, F32 = ctypes.c_int64, ctypes.c_float
+        L.moe_ops_status.argtypes = [P]
+        L.moe_dispatch_workspace.argtypes = [I32, I32, I32]
+        L.moe_dispatch_workspace.restype = SZ
+        L.moe_dispatch_rows.argtypes = [P, I32, I32, I32, P, I32, I32, P, P, P, P, P, SZ, P]
+        L.moe_dispatch_rows_backward.argtypes = [P, I32, I32, P, I32, I32, I32, P, P]
+        L.moe_combine_weighted.argtypes = [P, I32, I32, P, P, I32, I32, I32, P, P, P]
+        L.moe_combine_weighted_backward.argtypes = [P, I32, P, I32, P, P, I32, I32, I32, P, P, P]
+        L.moe_block_norm.argtypes = [P, I32, P, I32, I32, I32, P, I32, P, F32, P, F32, P, P, P, P, P]
+        L.moe_block_norm_backward_workspace.argtypes = [I32, I32]
+        L.moe_block_norm_backward_workspace.restype = SZ
+        L.moe_block_norm_backward.argtypes = [P, P, P, I32, P, I32, I32, I32, P, P, P, P, I32, P, F32, P, P, P, P, P,
+                                              P, SZ, P]
+        L.moe_mx4_quantize.argtypes = [P, I32, I32, I32, I32, P, I32, I32, P, P, P]
+        L.moe_mx4_dequantize.argtypes = [P, P, I64, I32, P, I32, P]
+        L.moe_mx4_matmul.argtypes = [P, P, I32, I32, P, P, I32, I32, P, P, I32, P]
+        for n in ("moe_ops_status", "moe_dispatch_rows", "moe_dispatch_rows_backward", "moe_combine_weighted",
+                  "moe_combine_weighted_backward", "moe_block_norm", "moe_block_norm_backward", "moe_mx4_quantize",
+                  "moe_mx4_dequantize", "moe_mx4_matmul"):
+            getattr(L, n).restype = ctypes.c_int
         for n in ("moe_create", "moe_forward", "moe_forward_host", "moe_forward_host_async", "moe_route", "moe_status",
                   "moe_debug_copy", "moe_profile_enable", "moe_profile_read", "moe_route_static",
                   "moe_forward_routed", "moe_combine_rows"):

@@ -187,27 +187,10 @@ int validate_config(const moe_config* c) {
     return MOE_OK;
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn get_encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
 // 2-D 16-bit row-major [rows, cols] tensor, box {64 columns, box_rows rows}, 128-byte swizzle.
 int encode_rows_map(CUtensorMap* m, const void* base, int rows, int cols, int box_rows,
                     CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_FLOAT16) {
-    EncodeTiledFn fn = get_encode_fn();
+    EncodeTiledFn fn = tensor_map_encode_fn();
     if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
@@ -223,6 +206,20 @@ int encode_rows_map(CUtensorMap* m, const void* base, int rows, int cols, int bo
 }  // namespace
 
 void moe::set_last_error(const char* msg) { g_last_error = msg; }
+
+// cuTensorMapEncodeTiled, looked up once (NULL if the driver has none).
+moe::EncodeTiledFn moe::tensor_map_encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
 
 constexpr int kProfCalls = 1024;
 constexpr int kProfEvents = 9;  // at most 8 kernels per call + the leading event

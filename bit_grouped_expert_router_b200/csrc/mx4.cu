@@ -1,0 +1,491 @@
+// mx4.cu -- microscaled 4-bit floating point (MXFP4): rows quantised, read back, and multiplied by
+// each expert's matrix on the tensor cores in that form.
+//
+// Blocks of 32 values along a row share a scale 2^(s - 127); each value is a 4-bit E2M1 number times
+// it.  The product's operands go to the tensor core as they are stored: kind::mxf4 multiplies the
+// 4-bit values and applies both scales per 32 columns, accumulating in fp32.
+#include "ops_common.cuh"
+
+namespace moe {
+
+namespace {
+
+// ---- quantisation ---------------------------------------------------------------------------------
+// Four neighbouring threads share a block of 32 values, eight each: 16-byte loads, the block's largest
+// magnitude by two exchanges, four bytes of codes per thread.  With pos, a token is read and quantised
+// once and written to all of its k rows, so the pass costs the bytes of x once and of the 4-bit rows.
+
+// Eight values as E2M1 codes (round to nearest, ties to even, magnitudes above 6 to 6), the first in
+// the low four bits.
+__device__ __forceinline__ uint32_t e2m1_pack(const float (&v)[8]) {
+    uint32_t w;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(w)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return w;
+}
+
+template <typename T, bool SWIGLU>
+__global__ void __launch_bounds__(256) mx4_quantize_kernel(Mx4QuantArgs a) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int n = a.K / 8;   // pieces of eight values; a multiple of 4
+    const int per = min(n, 256), rows = 256 / per, r = threadIdx.x / per;
+    const long long t = (long long)blockIdx.x * rows + r;
+    const bool live = r < rows && t < a.T;
+    const T* x = static_cast<const T*>(a.x) + (live ? (size_t)t * a.K * (SWIGLU ? 2 : 1) : 0);
+    // every thread makes every pass, so the exchanges below always have their whole warp
+    for (int c0 = 0; c0 < n; c0 += per) {
+        const int c = c0 + threadIdx.x - r * per;
+        const bool on = live && c < n;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+        if (on) {
+            Vec<T, 8> g;
+            g.load(x + c * 8);
+            if constexpr (SWIGLU) {
+                Vec<T, 8> u;
+                u.load(x + a.K + c * 8);
+                float uf[8];
+                g.get(v);
+                u.get(uf);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = v[i] / (1.f + expf(-v[i])) * uf[i];
+            } else {
+                g.get(v);
+            }
+        }
+        // magnitudes order like their bits, infinities and NaN above all finite ones
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // s - 127 = exponent of the largest magnitude - 2, at least -127; 2^(127 - s) is exact
+        const bool bad = top >= 0x7F800000u;
+        const int s = bad ? 255 : max((int)(top >> 23) - 2, 0);
+        const float up = __uint_as_float((uint32_t)(254 - s) << 23);
+        uint32_t w = 0;
+        if (!bad) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= up;
+            w = e2m1_pack(v);
+        }
+        if (!on) continue;
+        if (!a.pos) {
+            reinterpret_cast<uint32_t*>(a.codes)[(size_t)t * n + c] = w;
+            if ((c & 3) == 0) a.scales[(size_t)t * (n / 4) + c / 4] = (uint8_t)s;
+            continue;
+        }
+        for (int j0 = 0; j0 < a.k; j0 += 8) {
+            int p[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                p[u] = j0 + u < a.k ? a.pos[(size_t)t * a.k + j0 + u] : -1;
+                if (p[u] >= a.n_rows) {
+                    set_status(g_ops_status, MOE_STATUS_BOUNDS);
+                    p[u] = -1;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (p[u] < 0) continue;
+                reinterpret_cast<uint32_t*>(a.codes)[(size_t)p[u] * n + c] = w;
+                if ((c & 3) == 0) a.scales[(size_t)p[u] * (n / 4) + c / 4] = (uint8_t)s;
+            }
+        }
+    }
+}
+
+// ---- values ---------------------------------------------------------------------------------------
+template <typename T>
+__global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t* __restrict__ codes,
+                                                             const uint8_t* __restrict__ scales, size_t pieces,
+                                                             T* __restrict__ out) {
+    griddep_wait();
+    griddep_launch_dependents();
+    for (size_t i = blockIdx.x * (size_t)256 + threadIdx.x; i < pieces; i += (size_t)gridDim.x * 256) {
+        const uint32_t w = codes[i];
+        const uint32_t s = scales[i / 4];
+        // 2^(s - 127): a subnormal for s = 0, NaN for s = 255
+        const float scale = __uint_as_float(s == 255u ? 0x7FFFFFFFu : s ? s << 23 : 0x00400000u);
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            // E2M1 bits as the top of an fp32: sign, then exponent and mantissa in places 24..22 of a
+            // number scaled by 2^-126; the product by 2^126 is exact for the subnormal codes too
+            const uint32_t c = w >> (4 * j);
+            const float m = __uint_as_float(((c & 8u) << 28) | ((c & 7u) << 22)) * 0x1p126f;
+            v[j] = m * scale;
+        }
+        Vec<T, 8> o;
+        o.set(v);
+        o.store(out + i * 8);
+    }
+}
+
+// ---- grouped product ------------------------------------------------------------------------------
+// Work unit = 128 output features x up to 224 rows of one expert.  The weights are the M = 128
+// operand and the rows the N operand, so a short segment costs a narrow instruction (N = 16 and up)
+// instead of a padded one.  A persistent CTA walks units; per step of 256 columns
+//   warp 0       TMA: the 128 x 128-byte weight tile and the row tile (boxes of 32 rows), 128-byte swizzle
+//   warps 8-11   the scales: one stage of the ring each; a thread gathers the step's eight scale bytes of
+//                its rows and writes them in the order tcgen05.cp wants (512 bytes per 128 rows and
+//                128 columns: row r at 16 (r % 32) + 4 (r / 32))
+//   warp 1       tcgen05.cp of the scales to tensor memory, then four MMAs of 64 columns
+//   warps 4-7    epilogue of the unit before: tensor memory -> shared memory -> 16-byte row stores
+// Tensor memory: two accumulators of 224 columns (the epilogue of one overlaps the MMAs of the next) and
+// 2 x 32 columns of scales, alternating by step.
+constexpr int kTM = 128;             // features per unit
+constexpr int kTN = 224;             // most rows per unit
+constexpr int kStep = 256;           // columns per step: 128 bytes of codes per row
+constexpr int kRing = 4;
+constexpr int kABytes = kTM * 128;
+constexpr int kBBytes = kTN * 128;
+constexpr int kSfBytes = 2 * (512 + 2 * 512);   // per 128 columns: 512 B of weight scales, 2 x 512 B of row scales
+constexpr int kStageBytes = kABytes + kBBytes + kSfBytes;
+constexpr int kThreadsMm = 384;
+constexpr int kTmemSf = 448;         // first tensor-memory column of the scales
+constexpr int kOutRows = 32;         // rows per epilogue chunk
+
+template <typename T> struct Mx4Cfg {
+    static constexpr int kOutPitch = kTM * (int)sizeof(T) + 16;
+    static constexpr int kSmem = 1024 + kRing * kStageBytes + 2 * kOutRows * kOutPitch;
+};
+
+struct Unit {
+    int e, mt, row0, rows;   // expert, feature tile, first row, rows (1..224)
+};
+
+// Unit u of the list (experts in order, row tiles within an expert, feature tiles within a row tile):
+// a segment's 16-row groups are dealt evenly over its tiles.
+__device__ __forceinline__ Unit find_unit(int u, const int* ustart, const int* seg, const int* len, int E, int MT) {
+    int lo = 0, hi = E;   // ustart[lo] <= u < ustart[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (ustart[mid] <= u) lo = mid;
+        else hi = mid;
+    }
+    const int n = len[lo], groups = (n + 15) / 16, tiles = (n + kTN - 1) / kTN;
+    const int v = u - ustart[lo], tile = v / MT;
+    const int g0 = (int)((long long)groups * tile / tiles), g1 = (int)((long long)groups * (tile + 1) / tiles);
+    Unit r;
+    r.e = lo;
+    r.mt = v - tile * MT;
+    r.row0 = seg[lo] + 16 * g0;
+    r.rows = min(n, 16 * g1) - 16 * g0;
+    return r;
+}
+
+// 32 rows x 16 bytes of shared memory to 4 tensor-memory columns, repeated in all four lane quarters.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// Descriptor of a 512-byte scale block: no swizzle, 8-row groups of 16-byte rows 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t smem_addr) {
+    return (uint64_t)((smem_addr & 0x3FFFFu) >> 4) | ((uint64_t)(128u >> 4) << 16) | ((uint64_t)(128u >> 4) << 32) |
+           ((uint64_t)1u << 46);
+}
+// D (+)= A B with block scales: E2M1 operands, one E8M0 scale per 32 columns, 64 columns.
+__device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptor of kind::mxf4: bits 4-5 scale bytes of B (0: bytes 0-1, 2: bytes 2-3 of the
+// scale word), 7-9 and 10-11 operand types (1 = E2M1), 17-22 N / 8, 23 scale type (1 = E8M0),
+// 24-28 M / 16, 29-30 scale bytes of A.
+__device__ __forceinline__ uint32_t idesc_mx4(int n, uint32_t sf) {
+    return (sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(kTM >> 4) << 24) |
+           (sf << 29);
+}
+
+// The scale bytes of columns 256 ks .. 256 ks + 255 of one row (nk = K / 32 bytes long; zeros behind
+// its end): one 8-byte load where rows keep that alignment, two of 4 or single bytes where not.
+__device__ __forceinline__ uint2 load_scales(const uint8_t* row, int ks, int nk, int align) {
+    const int b = ks * 8;
+    uint2 v = make_uint2(0u, 0u);
+    if (align == 8) return *reinterpret_cast<const uint2*>(row + b);
+    if (align == 4) {
+        v.x = *reinterpret_cast<const uint32_t*>(row + b);
+        if (b + 4 < nk) v.y = *reinterpret_cast<const uint32_t*>(row + b + 4);
+        return v;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (b + i < nk) (i < 4 ? v.x : v.y) |= (uint32_t)row[b + i] << (8 * (i & 3));
+    return v;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs a, const __grid_constant__ CUtensorMap tm_w,
+                                                                   const __grid_constant__ CUtensorMap tm_x) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t full[kRing], empty[kRing], dfull[2], dempty[2], drain;
+    __shared__ int ustart[257], seg[256], len[256], wsum[8];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_word;
+    uint8_t* ring = smem_raw + (1024u - (smem_u32(smem_raw) & 1023u) & 1023u);
+    uint8_t* out = ring + kRing * kStageBytes;
+    volatile int* abort_flag = &abort_word;
+    uint32_t* status = g_ops_status;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = lane_id();
+
+    if (tid == 0) {
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&full[i], 2);    // the TMA thread and the stage's scale warp
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&dfull[i], 1);
+            mbar_init(&dempty[i], 4);
+        }
+        mbar_init(&drain, 1);
+        abort_word = 0;
+        fence_mbar_init();
+        prefetch_tmap(&tm_w);
+        prefetch_tmap(&tm_x);
+    }
+    if (warp == 2) {
+        tmem_alloc(&tmem_slot, 512);
+        tmem_relinquish();
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    // the unit list: segments held to [0, R], row tiles per expert, first unit of each expert
+    const int MT = (a.N + kTM - 1) / kTM;
+    int mine = 0, inc = 0;
+    if (tid < 256) {
+        if (tid < a.E) {
+            const int o0 = a.offsets[tid], o1 = a.offsets[tid + 1];
+            const int s0 = min(max(o0, 0), a.R), s1 = min(max(o1, s0), a.R);
+            if (blockIdx.x == 0 && (s0 != o0 || s1 != o1)) set_status(status, MOE_STATUS_BOUNDS);
+            seg[tid] = s0;
+            len[tid] = s1 - s0;
+            mine = (s1 - s0 + kTN - 1) / kTN * MT;
+        }
+        inc = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += o;
+        }
+        if (lane == 31) wsum[warp] = inc;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid < 256) {
+        for (int w = 0; w < warp; ++w) inc += wsum[w];
+        if (tid < a.E) ustart[tid] = inc - mine;
+        if (tid == a.E - 1) ustart[a.E] = inc;
+    }
+    __syncthreads();
+    const uint32_t tmem = tmem_slot;
+    const int total = ustart[a.E];
+    const int KS = (a.K + kStep - 1) / kStep;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            uint32_t it = 0;
+            for (int u = blockIdx.x; u < total; u += gridDim.x) {
+                const Unit un = find_unit(u, ustart, seg, len, a.E, MT);
+                const int boxes = (un.rows + kMx4BoxRows - 1) / kMx4BoxRows;
+                for (int ks = 0; ks < KS; ++ks, ++it) {
+                    const int s = it % kRing;
+                    if (!mbar_wait(&empty[s], ((it / kRing) & 1u) ^ 1u, abort_flag, status)) goto producer_done;
+                    uint8_t* st = ring + s * kStageBytes;
+                    mbar_arrive_expect_tx(&full[s], kABytes + boxes * kMx4BoxRows * 128);
+                    tma_load_2d(st, &tm_w, ks * 128, un.e * a.N + un.mt * kTM, &full[s]);
+                    for (int b = 0; b < boxes; ++b)
+                        tma_load_2d(st + kABytes + b * kMx4BoxRows * 128, &tm_x, ks * 128, un.row0 + b * kMx4BoxRows, &full[s]);
+                }
+            }
+        producer_done:
+            // every copy issued must land before the CTA may exit (bounded: after an abort the scale
+            // warps may have left without their arrivals)
+            for (uint32_t i = it > (uint32_t)kRing ? it - kRing : 0u; i < it; ++i)
+                mbar_drain(&full[i % kRing], (i / kRing) & 1u);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            uint32_t it = 0, tl = 0;
+            bool issued = false;
+            for (int u = blockIdx.x; u < total; u += gridDim.x, ++tl) {
+                const Unit un = find_unit(u, ustart, seg, len, a.E, MT);
+                const int n = (un.rows + 15) / 16 * 16;
+                const uint32_t ab = tl & 1u;
+                if (!mbar_wait(&dempty[ab], ((tl >> 1) & 1u) ^ 1u, abort_flag, status)) goto mma_done;
+                tc_fence_after();
+                const uint32_t d = tmem + ab * kTN;
+                const uint32_t i0 = idesc_mx4(n, 0), i2 = idesc_mx4(n, 2);
+                for (int ks = 0; ks < KS; ++ks, ++it) {
+                    const int s = it % kRing;
+                    if (!mbar_wait(&full[s], (it / kRing) & 1u, abort_flag, status)) goto mma_done;
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(ring + s * kStageBytes);
+                    const uint32_t sf = st + kABytes + kBBytes;
+                    const uint32_t tsf = tmem + kTmemSf + (it & 1u) * 32;
+                    const int kmma = min(4, (a.K - ks * kStep + 63) / 64);
+                    for (int c = 0; c < (kmma + 1) / 2; ++c) {
+                        tmem_cp_scales(tsf + c * 4, scale_desc(sf + c * 512));
+                        tmem_cp_scales(tsf + 8 + c * 8, scale_desc(sf + 1024 + c * 1024));
+                        if (n > 128) tmem_cp_scales(tsf + 12 + c * 8, scale_desc(sf + 1024 + c * 1024 + 512));
+                    }
+                    const uint64_t ad = sdesc_sw128(st), bd = sdesc_sw128(st + kABytes);
+                    for (int kk = 0; kk < kmma; ++kk)
+                        mma_mx4(d, ad + 2 * kk, bd + 2 * kk, (kk & 1) ? i2 : i0, tsf + (kk >> 1) * 4,
+                                tsf + 8 + (kk >> 1) * 8, (ks | kk) != 0 ? 1u : 0u);
+                    issued = true;
+                    tc_commit(&empty[s]);
+                }
+                tc_commit(&dfull[ab]);
+            }
+        mma_done:
+            if (*abort_flag && issued) {
+                tc_commit(&drain);
+                mbar_drain(&drain, 0);
+            }
+        }
+    } else if (warp >= 8) {
+        // ------------------------------------------------------------------ scales
+        // Warp w serves stage w - 8 of the ring: every fourth step, its loads issued before the wait
+        // for the stage.
+        const int mys = warp - 8, nk = a.K / 32;
+        const int align = nk % 8 == 0 ? 8 : nk % 4 == 0 ? 4 : 1;
+        uint32_t it = 0;   // steps before the unit
+        for (int u = blockIdx.x; u < total; u += gridDim.x, it += KS) {
+            const Unit un = find_unit(u, ustart, seg, len, a.E, MT);
+            for (int ks = (mys - (int)(it % kRing) + kRing) % kRing; ks < KS; ks += kRing) {
+                uint2 wv[4], xv[7];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int f = un.mt * kTM + 32 * q + lane;
+                    wv[q] = f < a.N ? load_scales(a.w_scales + ((size_t)un.e * a.N + f) * nk, ks, nk, align) : make_uint2(0u, 0u);
+                }
+#pragma unroll
+                for (int q = 0; q < 7; ++q) {
+                    const int r = 32 * q + lane;
+                    xv[q] = r < un.rows ? load_scales(a.scales + (size_t)(un.row0 + r) * nk, ks, nk, align) : make_uint2(0u, 0u);
+                }
+                const uint32_t n = it + ks;
+                const bool ok = mbar_wait(&empty[mys], ((n / kRing) & 1u) ^ 1u, abort_flag, status);
+                if (!__all_sync(0xffffffffu, ok)) goto scales_done;
+                uint8_t* sf = ring + mys * kStageBytes + kABytes + kBBytes + lane * 16;
+                *reinterpret_cast<uint4*>(sf) = make_uint4(wv[0].x, wv[1].x, wv[2].x, wv[3].x);
+                *reinterpret_cast<uint4*>(sf + 512) = make_uint4(wv[0].y, wv[1].y, wv[2].y, wv[3].y);
+                *reinterpret_cast<uint4*>(sf + 1024) = make_uint4(xv[0].x, xv[1].x, xv[2].x, xv[3].x);
+                *reinterpret_cast<uint4*>(sf + 1536) = make_uint4(xv[4].x, xv[5].x, xv[6].x, 0u);
+                *reinterpret_cast<uint4*>(sf + 2048) = make_uint4(xv[0].y, xv[1].y, xv[2].y, xv[3].y);
+                *reinterpret_cast<uint4*>(sf + 2560) = make_uint4(xv[4].y, xv[5].y, xv[6].y, 0u);
+                fence_proxy_async_smem();   // generic-proxy stores -> visible to tcgen05.cp
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[mys]);
+            }
+        }
+    scales_done:;
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------------ epilogue
+        using C = Mx4Cfg<T>;
+        const int q = warp & 3, et = tid - 128;
+        constexpr int kPieces = kTM * (int)sizeof(T) / 16, kPer = 16 / (int)sizeof(T);
+        uint32_t tl = 0;
+        int buf = 0;
+        for (int u = blockIdx.x; u < total; u += gridDim.x, ++tl) {
+            const Unit un = find_unit(u, ustart, seg, len, a.E, MT);
+            const uint32_t ab = tl & 1u;
+            const bool ok = mbar_wait(&dfull[ab], (tl >> 1) & 1u, abort_flag, status);
+            if (named_bar_or(2, 128, !ok)) break;   // the four warps leave together
+            tc_fence_after();
+            const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + ab * kTN;
+            const int f0 = un.mt * kTM;
+            for (int c0 = 0; c0 < un.rows; c0 += kOutRows, buf ^= 1) {
+                uint32_t v[32];
+                tmem_ld32(taddr + c0, v);
+                uint8_t* st = out + buf * kOutRows * C::kOutPitch;
+#pragma unroll
+                for (int r = 0; r < 32; ++r) {
+                    T* at = reinterpret_cast<T*>(st + r * C::kOutPitch) + 32 * q + lane;
+                    if constexpr (sizeof(T) == 4) *at = __uint_as_float(v[r]);
+                    else *at = __float2bfloat16_rn(__uint_as_float(v[r]));
+                }
+                if (c0 + kOutRows >= un.rows) {   // the accumulator is read: the next unit's MMAs may have it
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&dempty[ab]);
+                }
+                named_bar(1, 128);   // (the other buffer's readers are done: they passed this barrier after reading)
+                for (int i = et; i < kOutRows * kPieces; i += 128) {
+                    const int r = i / kPieces, c = i % kPieces;
+                    if (c0 + r < un.rows && f0 + c * kPer < a.N)
+                        *reinterpret_cast<uint4*>(static_cast<T*>(a.y) + (size_t)(un.row0 + c0 + r) * a.N + f0 + c * kPer) =
+                            *reinterpret_cast<const uint4*>(st + r * C::kOutPitch + c * 16);
+                }
+            }
+        }
+    }
+
+    __syncthreads();
+    if (warp == 2) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_mx4_quantize(const Mx4QuantArgs& a, int dtype, cudaStream_t st) {
+    const int n = a.K / 8, rows = 256 / (n < 256 ? n : 256);
+    const dim3 grid((a.T + rows - 1) / rows);
+    return with_dtype(dtype, [&](auto t) {
+        using T = decltype(t);
+        return a.swiglu ? launch_pdl(mx4_quantize_kernel<T, true>, grid, dim3(256), 0, st, a)
+                        : launch_pdl(mx4_quantize_kernel<T, false>, grid, dim3(256), 0, st, a);
+    });
+}
+
+cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, long long rows, int K, void* out,
+                                  int dtype, int num_sms, cudaStream_t st) {
+    const size_t pieces = (size_t)rows * (K / 8), want = (pieces + 255) / 256, most = (size_t)num_sms * 32;
+    return with_dtype(dtype, [&](auto t) {
+        using T = decltype(t);
+        return launch_pdl(mx4_dequantize_kernel<T>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st,
+                          reinterpret_cast<const uint32_t*>(codes), scales, pieces, static_cast<T*>(out));
+    });
+}
+
+template <typename T>
+static cudaError_t launch_matmul(const Mx4MatmulArgs& a, const CUtensorMap& tm_w, const CUtensorMap& tm_x, int num_sms,
+                                 cudaStream_t st) {
+    const cudaError_t e = cudaFuncSetAttribute(mx4_matmul_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Mx4Cfg<T>::kSmem);
+    if (e != cudaSuccess) return e;
+    // at most one row tile per kTN rows and one more per expert that has rows
+    const long long tiles = (long long)a.R / kTN + (a.E < a.R ? a.E : a.R);
+    const long long units = tiles * ((a.N + kTM - 1) / kTM);
+    return launch_pdl(mx4_matmul_kernel<T>, dim3((unsigned)(units < num_sms ? units : num_sms)), dim3(kThreadsMm),
+                      Mx4Cfg<T>::kSmem, st, a, tm_w, tm_x);
+}
+
+cudaError_t launch_mx4_matmul(const Mx4MatmulArgs& a, const CUtensorMap& tm_w, const CUtensorMap& tm_x, int dtype,
+                              int num_sms, cudaStream_t st) {
+    if (dtype == MOE_DTYPE_BF16) return launch_matmul<__nv_bfloat16>(a, tm_w, tm_x, num_sms, st);
+    if (dtype == MOE_DTYPE_FP32) return launch_matmul<float>(a, tm_w, tm_x, num_sms, st);
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t mx4_take_status(uint32_t* host, cudaStream_t st) { return take_status(host, st); }
+
+}  // namespace moe

@@ -294,6 +294,129 @@ MOE_API int moe_route_static(const uint16_t *x, int32_t T, int32_t H, const floa
                              const float *router_bias, int32_t E, int32_t k, int32_t *idx,
                              float *gates, void *stream);
 
+/* ---- operators around the experts ---------------------------------------------------------------
+ * Source: no counterpart on the pages; what a model puts around this layer's expert products, in
+ * public form: rows sorted by expert and back, the norms before and after the block, and experts in
+ * microscaled 4-bit floating point.
+ *
+ * Conventions, where they differ from the top of this file.
+ *  - No handle: the calls run on the CURRENT device (all pointers belong to it) and on `stream`, own
+ *    no memory and keep nothing between calls.  Whatever scratch a call needs is the caller's
+ *    `workspace` (16-byte aligned, at least the size the matching *_workspace function gives; it need
+ *    not be cleared and holds nothing afterwards).  Calls may overlap on the device as long as their
+ *    buffers do not, and may be captured in CUDA graphs; replays of graphs that share a workspace or
+ *    an output must not overlap.
+ *  - Rows are densely packed, of H values with H % 8 == 0, in one of the MOE_DTYPE_* types; sums,
+ *    row factors, gates and norm weights are fp32; each result is rounded once, to nearest (ties to
+ *    even).  No sum uses atomics: equal inputs give equal bits.
+ *  - Buffers must not overlap unless said otherwise.  A call for zero rows is a no-op returning
+ *    MOE_OK (moe_dispatch_rows still writes its zero offsets).
+ *  - A bad value met on the device (MOE_ERR_DEVICE_BOUNDS) or a wait that ran out
+ *    (MOE_ERR_DEVICE_TIMEOUT) is kept in a status word per device, taken by moe_ops_status().
+ *  Errors of every call: INVALID_ARG (null or misaligned pointer, unsupported size or type),
+ *  UNSUPPORTED_DEVICE, CUDA. */
+#define MOE_DTYPE_BF16 0
+#define MOE_DTYPE_FP16 1
+#define MOE_DTYPE_FP32 2
+
+/* Synchronise `stream`, read and clear the current device's status word of these operators: MOE_OK,
+ * MOE_ERR_DEVICE_TIMEOUT, MOE_ERR_DEVICE_BOUNDS or MOE_ERR_CUDA.  Not for use while capturing. */
+MOE_API int moe_ops_status(void *stream);
+
+/* The (token, slot) pairs of idx[T, k] sorted by expert (stable: within an expert in pair order), and
+ * the token rows copied into that order:
+ *   offsets[E+1] int32   offsets[e] = pairs of experts < e; offsets[E] = pairs kept
+ *   perm[T*k] int32      perm[p] = t*k + j of the pair at place p; -1 for p >= offsets[E]
+ *   pos[T, k] int32      the inverse: the pair's place, -1 for a pair that is not kept
+ *   rows[T*k, H]         rows[pos[t, j]] = x[t]; rows behind offsets[E] are left as they are
+ * An idx entry below 0 is no expert (padding): its pair is not kept.  One >= E is not kept either and
+ * is reported (DEVICE_BOUNDS).  An expert may repeat within a token.  x and rows may both be NULL: the
+ * pairs are sorted only.  1 <= k <= 32, 1 <= E <= 256, T*k < 2^30.  offsets and perm agree with
+ * moe_route's for the same idx. */
+MOE_API size_t moe_dispatch_workspace(int32_t T, int32_t k, int32_t E);
+MOE_API int moe_dispatch_rows(const void *x, int32_t dtype, int32_t T, int32_t H, const int32_t *idx, int32_t k,
+                              int32_t E, void *rows, int32_t *offsets, int32_t *perm, int32_t *pos,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/* Its gradient: dx[t] = sum over j with pos[t, j] >= 0 of drows[pos[t, j]], in slot order; a pos entry
+ * >= n_rows is skipped and reported (DEVICE_BOUNDS). */
+MOE_API int moe_dispatch_rows_backward(const void *drows, int32_t dtype, int32_t n_rows, const int32_t *pos,
+                                       int32_t T, int32_t k, int32_t H, void *dx, void *stream);
+
+/* out[t] = base[t] + sum over j with pos[t, j] >= 0 of gates[t, j] * rows[pos[t, j]], in slot order, for
+ * rows[n_rows, H], base[T, H] (NULL: zeros) and gates[T, k] fp32.  A row is not read for a pair without
+ * a place, whatever its gate.  out may be base.  pos as in moe_dispatch_rows (>= n_rows: reported). */
+MOE_API int moe_combine_weighted(const void *rows, int32_t dtype, int32_t n_rows, const int32_t *pos,
+                                 const float *gates, int32_t T, int32_t k, int32_t H, const void *base, void *out,
+                                 void *stream);
+
+/* Its gradient (base's is dout itself):
+ *   drows[pos[t, j]] = gates[t, j] * dout[t]            rows without a pair are left as they are
+ *   dgates[t, j] fp32 = <dout[t], rows[pos[t, j]]>      0 for a pair without a place
+ * No two entries of pos may be equal (as in moe_dispatch_rows' pos).  drows may be rows. */
+MOE_API int moe_combine_weighted_backward(const void *dout, int32_t dtype, const void *rows, int32_t n_rows,
+                                          const int32_t *pos, const float *gates, int32_t T, int32_t k, int32_t H,
+                                          void *drows, float *dgates, void *stream);
+
+/* The residual add after a block and the norm before the next one, for h[T, H] (the residual stream,
+ * h_dtype) and y[T, H] (the block's output, y_dtype):
+ *   a  = y * r_post * w_post      r_post[t] = 1 / sqrt(mean(y[t]^2) + eps) if norm_post, else 1
+ *   h' = h + scale * gate[t] * a  -> h_out[T, H] (h_dtype)
+ *   n  = h' * r_pre * w_pre       r_pre[t] = 1 / sqrt(mean(h'[t]^2) + eps)  -> n_out[T, H] (y_dtype)
+ * with w_post[H], gate[T], w_pre[H] fp32, each of which may be NULL (ones).  y NULL: h' = h, the norm
+ * alone (y_dtype is n_out's type; w_post, gate and norm_post must be NULL and 0).  h_out, n_out, r_post and
+ * r_pre (fp32 [T]) may each be NULL to skip it (r_post only with norm_post).  n is taken from h' before
+ * its rounding.  h_dtype is y_dtype or MOE_DTYPE_FP32.  H <= 16384, eps >= 0.  h_out may be h, n_out
+ * may be y (or h with y NULL and equal types). */
+MOE_API int moe_block_norm(const void *h, int32_t h_dtype, const void *y, int32_t y_dtype, int32_t T, int32_t H,
+                           const float *w_post, int32_t norm_post, const float *gate, float scale,
+                           const float *w_pre, float eps, void *h_out, void *n_out, float *r_post, float *r_pre,
+                           void *stream);
+
+/* Its gradient, from dn[T, H] (the gradient of n_out, y_dtype; NULL: none) and dh_out[T, H] (that of h_out, h_dtype;
+ * NULL: none), with h_out, r_pre (needed with dn) and r_post (needed with norm_post) as the forward
+ * call left them.  Results, each NULL to skip it: dh[T, H] (h_dtype), dy[T, H] (y_dtype), dw_pre[H],
+ * dw_post[H], dgate[T] (fp32; dw_pre needs dn; dy, dw_post and dgate need y).  dh may be dh_out, dy may be dn. */
+MOE_API size_t moe_block_norm_backward_workspace(int32_t T, int32_t H);
+MOE_API int moe_block_norm_backward(const void *dn, const void *dh_out, const void *h_out, int32_t h_dtype,
+                                    const void *y, int32_t y_dtype, int32_t T, int32_t H, const float *r_pre,
+                                    const float *r_post, const float *w_pre, const float *w_post,
+                                    int32_t norm_post, const float *gate, float scale, void *dh, void *dy,
+                                    float *dw_pre, float *dw_post, float *dgate, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/* Rows in microscaled 4-bit floating point (the OCP Microscaling Formats specification 1.0, MXFP4): blocks of
+ * 32 values along the row share a scale 2^(s - 127) (E8M0), each value is one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 with a
+ * sign (E2M1: bit 3 sign, bits 2-1 exponent, bit 0 mantissa) times it.  codes uint8 [rows, K/2], the even element of a
+ * pair in the low four bits; scales uint8 [rows, K/32].  K % 32 == 0.
+ * Quantisation: s - 127 = floor(log2(largest magnitude)) - 2 held to >= -127 (a block of zeros: s = 0),
+ * values rounded to nearest, ties to the even code, magnitudes above 6 to 6, signs of zeros kept; a
+ * block that holds an infinity or NaN gets s = 255 (NaN) and codes 0.
+ *   act MOE_ACT_NONE    v = x[t] for x[T, K]
+ *   act MOE_ACT_SWIGLU  v = silu(gate) * up in fp32 for x[T, 2K] = [gate | up]: the expert's activation
+ * pos NULL: row t goes to row t (n_rows >= T); else to the rows pos[t, j], j < k, where pos[t, j] >= 0
+ * (pos as in moe_dispatch_rows: the dispatch and the quantisation in one pass; >= n_rows: reported).
+ * Other rows are left as they are.  K <= 65536. */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_SWIGLU 1
+MOE_API int moe_mx4_quantize(const void *x, int32_t dtype, int32_t T, int32_t K, int32_t act, const int32_t *pos,
+                             int32_t k, int32_t n_rows, uint8_t *codes, uint8_t *scales, void *stream);
+
+/* The values that codes and scales stand for, rounded to out's type (exact in bf16 and fp32). */
+MOE_API int moe_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int32_t K, void *out,
+                               int32_t dtype, void *stream);
+
+/* Grouped product over rows sorted by expert: for e < E and offsets[e] <= r < offsets[e+1]
+ *   y[r, n] = sum_k x[r, k] * w_e[n, k]         fp32 sums, y in bf16 or fp32 (dtype)
+ * with x (codes[n_rows, K/2], scales[n_rows, K/32]) and w (w_codes[E, N, K/2], w_scales[E, N, K/32]) in
+ * microscaled 4-bit form and offsets[E+1] int32 on the device (as moe_dispatch_rows and moe_route write
+ * them).  Rows outside every segment are left as they are.  Offsets that decrease or leave
+ * [0, n_rows] are held to that range and reported (DEVICE_BOUNDS).  K % 32 == 0, N % 8 == 0,
+ * 1 <= E <= 256, E * N < 2^31. */
+MOE_API int moe_mx4_matmul(const uint8_t *codes, const uint8_t *scales, int32_t n_rows, int32_t K,
+                           const uint8_t *w_codes, const uint8_t *w_scales, int32_t E, int32_t N,
+                           const int32_t *offsets, void *y, int32_t dtype, void *stream);
+
 /* Source: library convenience (no passage).
  * Library version as major*10000 + minor*100 + patch. */
 MOE_API int moe_version(void);
