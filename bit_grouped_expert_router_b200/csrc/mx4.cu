@@ -135,11 +135,11 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t* __r
 // operand and the rows the N operand, so a short segment costs a narrow instruction (N = 16 and up)
 // instead of a padded one.  A persistent CTA walks units; per step of 256 columns
 //   warp 0       TMA: the 128 x 128-byte weight tile and the row tile (boxes of 32 rows), 128-byte swizzle
-//   warps 8-11   the scales: one stage of the ring each; a thread gathers the step's eight scale bytes of
-//                its rows and writes them in the order tcgen05.cp wants (512 bytes per 128 rows and
-//                128 columns: row r at 16 (r % 32) + 4 (r / 32))
+//   warps 8-11   the scales: a thread loads those of its rows 32 bytes at a time, ahead of their use, and writes
+//                each step's eight in the order tcgen05.cp wants (512 bytes per 128 rows and 128
+//                columns: row r at 16 (r % 32) + 4 (r / 32))
 //   warp 1       tcgen05.cp of the scales to tensor memory, then four MMAs of 64 columns
-//   warps 4-7    epilogue of the unit before: tensor memory -> shared memory -> 16-byte row stores
+//   warps 4-7, 12-15  epilogue of the unit before: tensor memory -> shared memory -> row stores
 // Tensor memory: two accumulators of 224 columns (the epilogue of one overlaps the MMAs of the next) and
 // 2 x 32 columns of scales, alternating by step.
 constexpr int kTM = 128;             // features per unit
@@ -150,14 +150,10 @@ constexpr int kABytes = kTM * 128;
 constexpr int kBBytes = kTN * 128;
 constexpr int kSfBytes = 2 * (512 + 2 * 512);   // per 128 columns: 512 B of weight scales, 2 x 512 B of row scales
 constexpr int kStageBytes = kABytes + kBBytes + kSfBytes;
-constexpr int kThreadsMm = 384;
+constexpr int kThreadsMm = 512;
 constexpr int kTmemSf = 448;         // first tensor-memory column of the scales
-constexpr int kOutRows = 32;         // rows per epilogue chunk
-
-template <typename T> struct Mx4Cfg {
-    static constexpr int kOutPitch = kTM * (int)sizeof(T) + 16;
-    static constexpr int kSmem = 1024 + kRing * kStageBytes + 2 * kOutRows * kOutPitch;
-};
+constexpr int kOutPitch = kTM * 2 + 16, kOutBytes = 32 * kOutPitch;   // a bf16 chunk of the epilogue
+constexpr int kSmemMm = 1024 + kRing * kStageBytes + 4 * kOutBytes;
 
 struct Unit {
     int e, mt, row0, rows;   // expert, feature tile, first row, rows (1..224)
@@ -165,7 +161,8 @@ struct Unit {
 
 // Unit u of the list (experts in order, row tiles within an expert, feature tiles within a row tile):
 // a segment's 16-row groups are dealt evenly over its tiles.
-__device__ __forceinline__ Unit find_unit(int u, const int* ustart, const int* seg, const int* len, int E, int MT) {
+__device__ __forceinline__ Unit find_unit(int u, const int* ustart, const int* seg, const int* len, int E, int MT,
+                                          bool whole_warp = false) {
     int lo = 0, hi = E;   // ustart[lo] <= u < ustart[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -174,18 +171,38 @@ __device__ __forceinline__ Unit find_unit(int u, const int* ustart, const int* s
     }
     const int n = len[lo], groups = (n + 15) / 16, tiles = (n + kTN - 1) / kTN;
     const int v = u - ustart[lo], tile = v / MT;
-    const int g0 = (int)((long long)groups * tile / tiles), g1 = (int)((long long)groups * (tile + 1) / tiles);
+    const int each = groups / tiles, left = groups - each * tiles;   // the first `left` tiles have one group more
+    const int g0 = each * tile + min(tile, left), g1 = g0 + each + (tile < left ? 1 : 0);
     Unit r;
     r.e = lo;
     r.mt = v - tile * MT;
     r.row0 = seg[lo] + 16 * g0;
     r.rows = min(n, 16 * g1) - 16 * g0;
+    if (whole_warp) {   // values that the compiler may keep in uniform registers
+        r.e = __shfl_sync(0xffffffffu, r.e, 0);
+        r.mt = __shfl_sync(0xffffffffu, r.mt, 0);
+        r.row0 = __shfl_sync(0xffffffffu, r.row0, 0);
+        r.rows = __shfl_sync(0xffffffffu, r.rows, 0);
+    }
     return r;
 }
 
+// The asynchronous instructions below are issued by one lane (`lead`) of a warp that runs their code
+// as a whole: under a branch on the lane the compiler moves every operand from vector to uniform
+// registers first, which cost about 100 cycles an MMA (measured: 4 MMAs of N = 128 in 453 cycles, 254
+// this way; the tensor core itself needs 256).
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
 // 32 rows x 16 bytes of shared memory to 4 tensor-memory columns, repeated in all four lane quarters.
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+        "l"(desc), "r"(lead)
+        : "memory");
 }
 // Descriptor of a 512-byte scale block: no swizzle, 8-row groups of 16-byte rows 128 bytes apart.
 __device__ __forceinline__ uint64_t scale_desc(uint32_t smem_addr) {
@@ -194,11 +211,34 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t smem_addr) {
 }
 // D (+)= A B with block scales: E2M1 operands, one E8M0 scale per 32 columns, 64 columns.
 __device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
-                                        uint32_t accumulate) {
+                                        uint32_t accumulate, uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 e, %7, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void commit_lead(uint64_t* bar, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void expect_lead(uint64_t* bar, uint32_t bytes, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
+        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+        "r"(bytes), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void tma_lead(uint32_t smem_dst, const CUtensorMap* map, int x, int y, uint64_t* bar,
+                                         uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+        "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];\n\t}" ::"r"(smem_dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)), "r"(lead)
         : "memory");
 }
 // Instruction descriptor of kind::mxf4: bits 4-5 scale bytes of B (0: bytes 0-1, 2: bytes 2-3 of the
@@ -209,21 +249,27 @@ __device__ __forceinline__ uint32_t idesc_mx4(int n, uint32_t sf) {
            (sf << 29);
 }
 
-// The scale bytes of columns 256 ks .. 256 ks + 255 of one row (nk = K / 32 bytes long; zeros behind
-// its end): one 8-byte load where rows keep that alignment, two of 4 or single bytes where not.
-__device__ __forceinline__ uint2 load_scales(const uint8_t* row, int ks, int nk, int align) {
-    const int b = ks * 8;
-    uint2 v = make_uint2(0u, 0u);
-    if (align == 8) return *reinterpret_cast<const uint2*>(row + b);
-    if (align == 4) {
-        v.x = *reinterpret_cast<const uint32_t*>(row + b);
-        if (b + 4 < nk) v.y = *reinterpret_cast<const uint32_t*>(row + b + 4);
-        return v;
-    }
+// 32 scale bytes of one row (1024 columns) from byte b on, zeros behind the row's end (nk = K / 32
+// bytes): 16-byte loads where rows keep that alignment, narrower ones where not.
+__device__ __forceinline__ void load_scales(uint32_t (&v)[8], const uint8_t* row, int b, int nk, int align) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (b + i < nk) (i < 4 ? v.x : v.y) |= (uint32_t)row[b + i] << (8 * (i & 3));
-    return v;
+    for (int i = 0; i < 8; ++i) v[i] = 0u;
+    if (align == 16) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (b + 16 * i < nk) {
+                const uint4 q = *reinterpret_cast<const uint4*>(row + b + 16 * i);
+                v[4 * i] = q.x; v[4 * i + 1] = q.y; v[4 * i + 2] = q.z; v[4 * i + 3] = q.w;
+            }
+    } else if (align == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (b + 4 * i < nk) v[i] = *reinterpret_cast<const uint32_t*>(row + b + 4 * i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (b + i < nk) v[i / 4] |= (uint32_t)row[b + i] << (8 * (i & 3));
+    }
 }
 
 template <typename T>
@@ -238,16 +284,16 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
     uint8_t* out = ring + kRing * kStageBytes;
     volatile int* abort_flag = &abort_word;
     uint32_t* status = g_ops_status;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = lane_id();
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = lane_id();
 
     if (tid == 0) {
         for (int i = 0; i < kRing; ++i) {
-            mbar_init(&full[i], 2);    // the TMA thread and the stage's scale warp
+            mbar_init(&full[i], 5);    // the TMA thread and the four scale warps
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&dfull[i], 1);
-            mbar_init(&dempty[i], 4);
+            mbar_init(&dempty[i], 8);
         }
         mbar_init(&drain, 1);
         abort_word = 0;
@@ -290,149 +336,191 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
         if (tid == a.E - 1) ustart[a.E] = inc;
     }
     __syncthreads();
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);   // (uniform, to the compiler too)
     const int total = ustart[a.E];
     const int KS = (a.K + kStep - 1) / kStep;
 
     if (warp == 0) {
         // ------------------------------------------------------------------ TMA producer
-        if (lane == 0) {
-            uint32_t it = 0;
-            for (int u = blockIdx.x; u < total; u += gridDim.x) {
-                const Unit un = find_unit(u, ustart, seg, len, a.E, MT);
-                const int boxes = (un.rows + kMx4BoxRows - 1) / kMx4BoxRows;
-                for (int ks = 0; ks < KS; ++ks, ++it) {
-                    const int s = it % kRing;
-                    if (!mbar_wait(&empty[s], ((it / kRing) & 1u) ^ 1u, abort_flag, status)) goto producer_done;
-                    uint8_t* st = ring + s * kStageBytes;
-                    mbar_arrive_expect_tx(&full[s], kABytes + boxes * kMx4BoxRows * 128);
-                    tma_load_2d(st, &tm_w, ks * 128, un.e * a.N + un.mt * kTM, &full[s]);
-                    for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(st + kABytes + b * kMx4BoxRows * 128, &tm_x, ks * 128, un.row0 + b * kMx4BoxRows, &full[s]);
-                }
+        const uint32_t lead = elect_lane();
+        uint32_t it = 0;
+        for (int u = blockIdx.x; u < total; u += gridDim.x) {
+            const Unit un = find_unit(u, ustart, seg, len, a.E, MT, true);
+            const int boxes = (un.rows + kMx4BoxRows - 1) / kMx4BoxRows, wrow = un.e * a.N + un.mt * kTM;
+            for (int ks = 0; ks < KS; ++ks, ++it) {
+                const int s = it % kRing;
+                const bool ok = mbar_wait(&empty[s], ((it / kRing) & 1u) ^ 1u, abort_flag, status);
+                if (!__all_sync(0xffffffffu, ok)) goto producer_done;
+                const uint32_t st = smem_u32(ring) + s * kStageBytes;
+                expect_lead(&full[s], kABytes + boxes * kMx4BoxRows * 128, lead);
+                tma_lead(st, &tm_w, ks * 128, wrow, &full[s], lead);
+                for (int b = 0; b < boxes; ++b)
+                    tma_lead(st + kABytes + b * kMx4BoxRows * 128, &tm_x, ks * 128, un.row0 + b * kMx4BoxRows, &full[s], lead);
             }
-        producer_done:
-            // every copy issued must land before the CTA may exit (bounded: after an abort the scale
-            // warps may have left without their arrivals)
-            for (uint32_t i = it > (uint32_t)kRing ? it - kRing : 0u; i < it; ++i)
-                mbar_drain(&full[i % kRing], (i / kRing) & 1u);
         }
+    producer_done:
+        // every copy issued must land before the CTA may exit (bounded: after an abort the scale
+        // warps may have left without their arrivals)
+        for (uint32_t i = it > (uint32_t)kRing ? it - kRing : 0u; i < it; ++i)
+            mbar_drain(&full[i % kRing], (i / kRing) & 1u);
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            uint32_t it = 0, tl = 0;
-            bool issued = false;
-            for (int u = blockIdx.x; u < total; u += gridDim.x, ++tl) {
-                const Unit un = find_unit(u, ustart, seg, len, a.E, MT);
-                const int n = (un.rows + 15) / 16 * 16;
-                const uint32_t ab = tl & 1u;
-                if (!mbar_wait(&dempty[ab], ((tl >> 1) & 1u) ^ 1u, abort_flag, status)) goto mma_done;
+        const uint32_t lead = elect_lane();
+        uint32_t it = 0, tl = 0;
+        bool issued = false;
+        for (int u = blockIdx.x; u < total; u += gridDim.x, ++tl) {
+            const Unit un = find_unit(u, ustart, seg, len, a.E, MT, true);
+            const int n = (un.rows + 15) / 16 * 16;
+            const uint32_t ab = tl & 1u;
+            bool ok = mbar_wait(&dempty[ab], ((tl >> 1) & 1u) ^ 1u, abort_flag, status);
+            if (!__all_sync(0xffffffffu, ok)) goto mma_done;
+            tc_fence_after();
+            const uint32_t d = tmem + ab * kTN;
+            const uint32_t i0 = idesc_mx4(n, 0), i2 = idesc_mx4(n, 2);
+            for (int ks = 0; ks < KS; ++ks, ++it) {
+                const int s = it % kRing;
+                ok = mbar_wait(&full[s], (it / kRing) & 1u, abort_flag, status);
+                if (!__all_sync(0xffffffffu, ok)) goto mma_done;
                 tc_fence_after();
-                const uint32_t d = tmem + ab * kTN;
-                const uint32_t i0 = idesc_mx4(n, 0), i2 = idesc_mx4(n, 2);
-                for (int ks = 0; ks < KS; ++ks, ++it) {
-                    const int s = it % kRing;
-                    if (!mbar_wait(&full[s], (it / kRing) & 1u, abort_flag, status)) goto mma_done;
-                    tc_fence_after();
-                    const uint32_t st = smem_u32(ring + s * kStageBytes);
-                    const uint32_t sf = st + kABytes + kBBytes;
-                    const uint32_t tsf = tmem + kTmemSf + (it & 1u) * 32;
-                    const int kmma = min(4, (a.K - ks * kStep + 63) / 64);
-                    for (int c = 0; c < (kmma + 1) / 2; ++c) {
-                        tmem_cp_scales(tsf + c * 4, scale_desc(sf + c * 512));
-                        tmem_cp_scales(tsf + 8 + c * 8, scale_desc(sf + 1024 + c * 1024));
-                        if (n > 128) tmem_cp_scales(tsf + 12 + c * 8, scale_desc(sf + 1024 + c * 1024 + 512));
-                    }
-                    const uint64_t ad = sdesc_sw128(st), bd = sdesc_sw128(st + kABytes);
-                    for (int kk = 0; kk < kmma; ++kk)
+                const uint32_t st = smem_u32(ring) + s * kStageBytes, sf = st + kABytes + kBBytes;
+                const uint32_t tsf = tmem + kTmemSf + (it & 1u) * 32;
+                const int kmma = min(4, (a.K - ks * kStep + 63) / 64);
+                for (int c = 0; c < (kmma + 1) / 2; ++c) {
+                    tmem_cp_scales(tsf + c * 4, scale_desc(sf + c * 512), lead);
+                    tmem_cp_scales(tsf + 8 + c * 8, scale_desc(sf + 1024 + c * 1024), lead);
+                    if (n > 128) tmem_cp_scales(tsf + 12 + c * 8, scale_desc(sf + 1024 + c * 1024 + 512), lead);
+                }
+                const uint64_t ad = sdesc_sw128(st), bd = sdesc_sw128(st + kABytes);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    if (kk < kmma)
                         mma_mx4(d, ad + 2 * kk, bd + 2 * kk, (kk & 1) ? i2 : i0, tsf + (kk >> 1) * 4,
-                                tsf + 8 + (kk >> 1) * 8, (ks | kk) != 0 ? 1u : 0u);
-                    issued = true;
-                    tc_commit(&empty[s]);
-                }
-                tc_commit(&dfull[ab]);
+                                tsf + 8 + (kk >> 1) * 8, (ks | kk) != 0 ? 1u : 0u, lead);
+                issued = true;
+                commit_lead(&empty[s], lead);
             }
-        mma_done:
-            if (*abort_flag && issued) {
-                tc_commit(&drain);
-                mbar_drain(&drain, 0);
-            }
+            commit_lead(&dfull[ab], lead);
         }
-    } else if (warp >= 8) {
+    mma_done:
+        if (*abort_flag && issued) {
+            commit_lead(&drain, lead);
+            mbar_drain(&drain, 0);
+        }
+    } else if (warp >= 8 && warp < 12) {
         // ------------------------------------------------------------------ scales
-        // Warp w serves stage w - 8 of the ring: every fourth step, its loads issued before the wait
-        // for the stage.
-        const int mys = warp - 8, nk = a.K / 32;
-        const int align = nk % 8 == 0 ? 8 : nk % 4 == 0 ? 4 : 1;
-        uint32_t it = 0;   // steps before the unit
-        for (int u = blockIdx.x; u < total; u += gridDim.x, it += KS) {
-            const Unit un = find_unit(u, ustart, seg, len, a.E, MT);
-            for (int ks = (mys - (int)(it % kRing) + kRing) % kRing; ks < KS; ks += kRing) {
-                uint2 wv[4], xv[7];
+        // Thread r has weight row r and token rows r and r + 128 of the unit.  It loads a row's scales
+        // a sector (1024 columns, four steps) at a time, the next sector before it hands out this one.
+        const int r = tid - 256, nk = a.K / 32;
+        const int align = nk % 16 == 0 ? 16 : nk % 4 == 0 ? 4 : 1;
+        uint32_t nxt[3][8] = {};
+        int u = blockIdx.x, ks0 = 0;
+        Unit un = {0, 0, 0, 0};
+        auto fetch = [&]() {
+            const int f = un.mt * kTM + r;
+            load_scales(nxt[0], a.w_scales + ((size_t)un.e * a.N + f) * nk, ks0 * 8, f < a.N ? nk : 0, align);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int f = un.mt * kTM + 32 * q + lane;
-                    wv[q] = f < a.N ? load_scales(a.w_scales + ((size_t)un.e * a.N + f) * nk, ks, nk, align) : make_uint2(0u, 0u);
-                }
+            for (int i = 0; i < 2; ++i) {
+                const int row = r + 128 * i;
+                load_scales(nxt[1 + i], a.scales + (size_t)(un.row0 + row) * nk, ks0 * 8, row < un.rows ? nk : 0, align);
+            }
+        };
+        const uint32_t at = (uint32_t)((r & 31) * 16 + (r >> 5) * 4);
+        uint32_t it = 0;
+        int steps = 0;   // of the sector at hand (none yet)
+        bool more = u < total;
+        if (more) un = find_unit(u, ustart, seg, len, a.E, MT);
+        while (more || steps > 0) {
+            uint32_t cur[3][8];
+            const int now = steps;
 #pragma unroll
-                for (int q = 0; q < 7; ++q) {
-                    const int r = 32 * q + lane;
-                    xv[q] = r < un.rows ? load_scales(a.scales + (size_t)(un.row0 + r) * nk, ks, nk, align) : make_uint2(0u, 0u);
+            for (int i = 0; i < 3; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) cur[i][j] = nxt[i][j];
+            steps = 0;
+            if (more) {
+                fetch();
+                steps = min(4, KS - ks0);
+                ks0 += 4;
+                if (ks0 >= KS) {
+                    ks0 = 0;
+                    u += gridDim.x;
+                    more = u < total;
+                    if (more) un = find_unit(u, ustart, seg, len, a.E, MT);
                 }
-                const uint32_t n = it + ks;
-                const bool ok = mbar_wait(&empty[mys], ((n / kRing) & 1u) ^ 1u, abort_flag, status);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (j >= now) break;
+                const int s = it % kRing;
+                const bool ok = mbar_wait(&empty[s], ((it / kRing) & 1u) ^ 1u, abort_flag, status);
                 if (!__all_sync(0xffffffffu, ok)) goto scales_done;
-                uint8_t* sf = ring + mys * kStageBytes + kABytes + kBBytes + lane * 16;
-                *reinterpret_cast<uint4*>(sf) = make_uint4(wv[0].x, wv[1].x, wv[2].x, wv[3].x);
-                *reinterpret_cast<uint4*>(sf + 512) = make_uint4(wv[0].y, wv[1].y, wv[2].y, wv[3].y);
-                *reinterpret_cast<uint4*>(sf + 1024) = make_uint4(xv[0].x, xv[1].x, xv[2].x, xv[3].x);
-                *reinterpret_cast<uint4*>(sf + 1536) = make_uint4(xv[4].x, xv[5].x, xv[6].x, 0u);
-                *reinterpret_cast<uint4*>(sf + 2048) = make_uint4(xv[0].y, xv[1].y, xv[2].y, xv[3].y);
-                *reinterpret_cast<uint4*>(sf + 2560) = make_uint4(xv[4].y, xv[5].y, xv[6].y, 0u);
+                uint8_t* sf = ring + s * kStageBytes + kABytes + kBBytes + at;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    *reinterpret_cast<uint32_t*>(sf + c * 512) = cur[0][2 * j + c];
+                    *reinterpret_cast<uint32_t*>(sf + 1024 + c * 1024) = cur[1][2 * j + c];
+                    *reinterpret_cast<uint32_t*>(sf + 1536 + c * 1024) = cur[2][2 * j + c];
+                }
                 fence_proxy_async_smem();   // generic-proxy stores -> visible to tcgen05.cp
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&full[mys]);
+                if (lane == 0) mbar_arrive(&full[s]);
+                ++it;
             }
         }
     scales_done:;
     } else if (warp >= 4) {
         // ------------------------------------------------------------------ epilogue
-        using C = Mx4Cfg<T>;
-        const int q = warp & 3, et = tid - 128;
-        constexpr int kPieces = kTM * (int)sizeof(T) / 16, kPer = 16 / (int)sizeof(T);
+        // Two groups of four warps take the unit's chunks of 32 rows in turn.  A thread holds one feature
+        // of the chunk's rows.  In bf16, the lanes of a pair swap halves so that each has two
+        // neighbouring features of every other row, and the chunk goes through shared memory to
+        // stores of whole 256-byte row pieces; the pair's two rows are 4 apart and the pitch is 272
+        // bytes, so a warp's 4-byte stores fall into different banks.  (The pair's values stored
+        // directly, 64 bytes a row: 162 us for 32768 x 2048 outputs of 512 columns, 108 us this way.)
+        const int q = warp & 3, grp = warp >= 12 ? 1 : 0, gt = tid & 127;
         uint32_t tl = 0;
         int buf = 0;
         for (int u = blockIdx.x; u < total; u += gridDim.x, ++tl) {
             const Unit un = find_unit(u, ustart, seg, len, a.E, MT);
             const uint32_t ab = tl & 1u;
             const bool ok = mbar_wait(&dfull[ab], (tl >> 1) & 1u, abort_flag, status);
-            if (named_bar_or(2, 128, !ok)) break;   // the four warps leave together
+            if (named_bar_or(1 + grp, 128, !ok)) break;   // the group leaves together
             tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + ab * kTN;
-            const int f0 = un.mt * kTM;
-            for (int c0 = 0; c0 < un.rows; c0 += kOutRows, buf ^= 1) {
+            const int f0 = un.mt * kTM, f = f0 + 32 * q + lane;
+            T* y = static_cast<T*>(a.y) + (size_t)un.row0 * a.N;
+            for (int c0 = 32 * grp; c0 < un.rows; c0 += 64) {
                 uint32_t v[32];
                 tmem_ld32(taddr + c0, v);
-                uint8_t* st = out + buf * kOutRows * C::kOutPitch;
+                if constexpr (sizeof(T) == 4) {
 #pragma unroll
-                for (int r = 0; r < 32; ++r) {
-                    T* at = reinterpret_cast<T*>(st + r * C::kOutPitch) + 32 * q + lane;
-                    if constexpr (sizeof(T) == 4) *at = __uint_as_float(v[r]);
-                    else *at = __float2bfloat16_rn(__uint_as_float(v[r]));
-                }
-                if (c0 + kOutRows >= un.rows) {   // the accumulator is read: the next unit's MMAs may have it
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&dempty[ab]);
-                }
-                named_bar(1, 128);   // (the other buffer's readers are done: they passed this barrier after reading)
-                for (int i = et; i < kOutRows * kPieces; i += 128) {
-                    const int r = i / kPieces, c = i % kPieces;
-                    if (c0 + r < un.rows && f0 + c * kPer < a.N)
-                        *reinterpret_cast<uint4*>(static_cast<T*>(a.y) + (size_t)(un.row0 + c0 + r) * a.N + f0 + c * kPer) =
-                            *reinterpret_cast<const uint4*>(st + r * C::kOutPitch + c * 16);
+                    for (int r = 0; r < 32; ++r)
+                        if (c0 + r < un.rows && f < a.N) y[(size_t)(c0 + r) * a.N + f] = __uint_as_float(v[r]);
+                } else {
+                    const bool odd = lane & 1;
+                    uint8_t* st = out + (grp * 2 + buf) * kOutBytes;
+                    uint8_t* at = st + (odd ? 4 * kOutPitch : 0) + (32 * q + (lane & ~1)) * 2;
+                    buf ^= 1;
+#pragma unroll
+                    for (int r8 = 0; r8 < 32; r8 += 8)
+#pragma unroll
+                        for (int r = r8; r < r8 + 4; ++r) {   // even lane: row r, odd lane: row r + 4
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v[r] : v[r + 4], 1);
+                            const float lo = __uint_as_float(odd ? got : v[r]), hi = __uint_as_float(odd ? v[r + 4] : got);
+                            *reinterpret_cast<__nv_bfloat162*>(at + r * kOutPitch) = __floats2bfloat162_rn(lo, hi);
+                        }
+                    named_bar(3 + grp, 128);   // (who writes a buffer again has passed the barrier behind its readers)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = i * 8 + (gt >> 4), c = (gt & 15) * 8;
+                        if (c0 + r < un.rows && f0 + c < a.N)
+                            *reinterpret_cast<uint4*>(y + (size_t)(c0 + r) * a.N + f0 + c) =
+                                *reinterpret_cast<const uint4*>(st + r * kOutPitch + c * 2);
+                    }
                 }
             }
+            tc_fence_before();   // the accumulator is read: the MMAs of the unit after the next may have it
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&dempty[ab]);
         }
     }
 
@@ -470,13 +558,13 @@ template <typename T>
 static cudaError_t launch_matmul(const Mx4MatmulArgs& a, const CUtensorMap& tm_w, const CUtensorMap& tm_x, int num_sms,
                                  cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(mx4_matmul_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               Mx4Cfg<T>::kSmem);
+                                               kSmemMm);
     if (e != cudaSuccess) return e;
     // at most one row tile per kTN rows and one more per expert that has rows
     const long long tiles = (long long)a.R / kTN + (a.E < a.R ? a.E : a.R);
     const long long units = tiles * ((a.N + kTM - 1) / kTM);
     return launch_pdl(mx4_matmul_kernel<T>, dim3((unsigned)(units < num_sms ? units : num_sms)), dim3(kThreadsMm),
-                      Mx4Cfg<T>::kSmem, st, a, tm_w, tm_x);
+                      kSmemMm, st, a, tm_w, tm_x);
 }
 
 cudaError_t launch_mx4_matmul(const Mx4MatmulArgs& a, const CUtensorMap& tm_w, const CUtensorMap& tm_x, int dtype,
