@@ -69,9 +69,11 @@ struct NormArgs {
     int T, H, norm_post;
     float scale, eps;
 };
+constexpr long long kNormManyValues = 1 << 20;   // from here on the rows alone fill the SMs
 cudaError_t launch_block_norm(const NormArgs& a, int h_dtype, int y_dtype, cudaStream_t st);
 
-constexpr int kNormBwdCtas = 592;   // most CTAs of the backward pass: one partial weight gradient each
+constexpr int kNormBwdCtas = 148;   // most blocks of the backward pass (one per SM)
+constexpr int kNormBwdStages = 4;   // most rows in flight per group of warps
 struct NormBwdArgs {
     const void* dn;
     const void* dh_out;
@@ -91,8 +93,9 @@ struct NormBwdArgs {
     int T, H, norm_post;
     float scale;
 };
-int norm_bwd_ctas(int T, int H);
+int norm_bwd_ctas(int T);
 cudaError_t launch_block_norm_bwd(const NormBwdArgs& a, int h_dtype, int y_dtype, cudaStream_t st);
+cudaError_t norm_take_status(uint32_t* host, cudaStream_t st);
 
 // ---- mx4.cu: microscaled 4-bit floating point ------------------------------------------------------
 struct Mx4QuantArgs {

@@ -100,12 +100,13 @@ int moe_ops_status(void* stream) {
     OPS_DEVICE(sms);
     (void)sms;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    uint32_t a = 0, b = 0;
+    uint32_t a = 0, b = 0, c = 0;
     cudaError_t e = rows_take_status(&a, st);
-    if (e == cudaSuccess) e = mx4_take_status(&b, st);
+    if (e == cudaSuccess) e = norm_take_status(&b, st);
+    if (e == cudaSuccess) e = mx4_take_status(&c, st);
     if (e != cudaSuccess) return launched("moe_ops_status", e);
-    if ((a | b) & MOE_STATUS_TIMEOUT) return fail(MOE_ERR_DEVICE_TIMEOUT, "a device-side wait timed out");
-    if ((a | b) & MOE_STATUS_BOUNDS) return fail(MOE_ERR_DEVICE_BOUNDS, "a device-side index check failed");
+    if ((a | b | c) & MOE_STATUS_TIMEOUT) return fail(MOE_ERR_DEVICE_TIMEOUT, "a device-side wait timed out");
+    if ((a | b | c) & MOE_STATUS_BOUNDS) return fail(MOE_ERR_DEVICE_BOUNDS, "a device-side index check failed");
     return MOE_OK;
 }
 
@@ -223,7 +224,7 @@ int moe_block_norm(const void* h, int32_t h_dtype, const void* y, int32_t y_dtyp
 
 size_t moe_block_norm_backward_workspace(int32_t T, int32_t H) {
     if (T < 0 || H < 8 || H % 8 != 0 || H > kMaxNormWidth) return 0;
-    return sizeof(float) * 2 * (size_t)norm_bwd_ctas(T, H) * H;
+    return sizeof(float) * 2 * (size_t)norm_bwd_ctas(T) * H;
 }
 
 int moe_block_norm_backward(const void* dn, const void* dh_out, const void* h_out, int32_t h_dtype, const void* y,

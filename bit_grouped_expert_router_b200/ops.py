@@ -116,16 +116,16 @@ def dispatch_rows(x, idx, E: int, rows=None) -> Dispatch:
         H, dt = _matrix(x, "x")[1], _dtype(x, "x")
         xp = _have(x, "x", x.dtype, (T, H), dev)
         if rows is None:
-            rows = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
+            rows = x.new_empty((T * k, H))
     elif rows is not None:
         raise ValueError("rows needs x")
     rp = None if rows is None else _have(rows, "rows", x.dtype, (T * k, H), dev)
-    offsets = torch.empty(max(E, 0) + 1, dtype=torch.int32, device=idx.device)
-    perm = torch.empty(T * k, dtype=torch.int32, device=idx.device)
-    pos = torch.empty((T, k), dtype=torch.int32, device=idx.device)
+    offsets = idx.new_empty(max(E, 0) + 1)
+    perm = idx.new_empty(T * k)
+    pos = idx.new_empty((T, k))
     L = M.lib()
     need = L.moe_dispatch_workspace(T, k, E)
-    ws = torch.empty(need, dtype=torch.uint8, device=idx.device) if need else None
+    ws = idx.new_empty(need // 4) if need else None
     M.check(L.moe_dispatch_rows(xp, dt, T, H, ip, k, E, rp, offsets.data_ptr(), perm.data_ptr(), pos.data_ptr(),
                                 None if ws is None else ws.data_ptr(), need, _stream(idx)))
     return Dispatch(rows, offsets, perm, pos)
@@ -141,7 +141,7 @@ def dispatch_rows_backward(drows, pos, out=None):
     dp = _have(drows, "drows", drows.dtype, (n, H), dev)
     pp = _have(pos, "pos", torch.int32, (T, k), dev)
     if out is None:
-        out = torch.empty((T, H), dtype=drows.dtype, device=drows.device)
+        out = drows.new_empty((T, H))
     op = _have(out, "out", drows.dtype, (T, H), dev)
     M.check(M.lib().moe_dispatch_rows_backward(dp, dt, n, pp, T, k, H, op, _stream(drows)))
     return out
@@ -159,7 +159,7 @@ def combine_weighted(rows, pos, gates, base=None, out=None):
     gp = _have(gates, "gates", torch.float32, (T, k), dev)
     bp = _have(base, "base", rows.dtype, (T, H), dev)
     if out is None:
-        out = torch.empty((T, H), dtype=rows.dtype, device=rows.device)
+        out = rows.new_empty((T, H))
     op = _have(out, "out", rows.dtype, (T, H), dev)
     M.check(M.lib().moe_combine_weighted(rp, dt, n, pp, gp, T, k, H, bp, op, _stream(rows)))
     return out
@@ -179,7 +179,7 @@ def combine_weighted_backward(dout, rows, pos, gates, drows=None):
     if drows is None:
         drows = torch.empty_like(rows)
     dp = _have(drows, "drows", rows.dtype, (n, H), dev)
-    dgates = torch.empty((T, k), dtype=torch.float32, device=rows.device)
+    dgates = gates.new_empty((T, k))
     M.check(M.lib().moe_combine_weighted_backward(op, dt, rp, n, pp, gp, T, k, H, dp, dgates.data_ptr(), _stream(rows)))
     return drows, dgates
 
@@ -205,10 +205,10 @@ def block_norm(h, y=None, w_pre=None, w_post=None, gate=None, scale: float = 1.0
     if y is not None and h_out is None:
         h_out = torch.empty_like(h)
     if pre and n_out is None:
-        n_out = torch.empty((T, H), dtype=nt, device=h.device)
+        n_out = h.new_empty((T, H), dtype=nt)
     op, np_ = _have(h_out, "h_out", h.dtype, (T, H), dev), _have(n_out, "n_out", nt, (T, H), dev)
-    r_post = torch.empty(T, dtype=torch.float32, device=h.device) if norm_post else None
-    r_pre = torch.empty(T, dtype=torch.float32, device=h.device) if pre else None
+    r_post = h.new_empty(T, dtype=torch.float32) if norm_post else None
+    r_pre = h.new_empty(T, dtype=torch.float32) if pre else None
     M.check(M.lib().moe_block_norm(hp, hd, yp, yd, T, H, wq, 1 if norm_post else 0, gp, scale, wp, eps, op, np_,
                                    None if r_post is None else r_post.data_ptr(),
                                    None if r_pre is None else r_pre.data_ptr(), _stream(h)))
@@ -235,12 +235,12 @@ def block_norm_backward(dn, dh_out, h_out, y=None, r_pre=None, r_post=None, w_pr
     gp = _have(gate, "gate", torch.float32, (T,), dev)
     dh = torch.empty_like(h_out)
     dy = torch.empty_like(y) if y is not None else None
-    dw_pre = torch.empty(H, dtype=torch.float32, device=h_out.device) if w_pre is not None else None
-    dw_post = torch.empty(H, dtype=torch.float32, device=h_out.device) if w_post is not None else None
-    dgate = torch.empty(T, dtype=torch.float32, device=h_out.device) if gate is not None else None
+    dw_pre = w_pre.new_empty(H) if w_pre is not None else None
+    dw_post = w_post.new_empty(H) if w_post is not None else None
+    dgate = gate.new_empty(T) if gate is not None else None
     L = M.lib()
     need = L.moe_block_norm_backward_workspace(T, H) if dw_pre is not None or dw_post is not None else 0
-    ws = torch.empty(need, dtype=torch.uint8, device=h_out.device) if need else None
+    ws = h_out.new_empty(need // 4, dtype=torch.float32) if need else None
     M.check(L.moe_block_norm_backward(np_, ip, hp, hd, yp, yd, T, H, rp, rq, wp, wq, 0 if r_post is None else 1, gp, scale,
                                       dh.data_ptr(), M._ptr(dy), M._ptr(dw_pre), M._ptr(dw_post), M._ptr(dgate),
                                       M._ptr(ws), need, _stream(h_out)))
@@ -263,9 +263,9 @@ def mx4_quantize(x, pos=None, act: Optional[str] = None, codes=None, scales=None
     pp = _have(pos, "pos", torch.int32, (T, k), dev)
     n = T * k if codes is None else _matrix(codes, "codes")[0]
     if codes is None:
-        codes = torch.empty((n, K // 2), dtype=torch.uint8, device=x.device)
+        codes = x.new_empty((n, K // 2), dtype=torch.uint8)
     if scales is None:
-        scales = torch.empty((n, K // 32), dtype=torch.uint8, device=x.device)
+        scales = x.new_empty((n, K // 32), dtype=torch.uint8)
     cp = _have(codes, "codes", torch.uint8, (n, K // 2), dev)
     sp = _have(scales, "scales", torch.uint8, (n, K // 32), dev)
     M.check(M.lib().moe_mx4_quantize(xp, _dtype(x, "x"), T, K, _ACTS[act], pp, k, n, cp, sp, _stream(x)))
@@ -281,7 +281,7 @@ def mx4_dequantize(codes, scales, dtype=torch.bfloat16):
     sp = _have(scales, "scales", torch.uint8, codes.shape[:-1] + (K // 32,), dev)
     if dtype not in _DTYPES:
         raise ValueError(f"dtype: bf16, fp16 or fp32 is needed, got {dtype}")
-    out = torch.empty(codes.shape[:-1] + (K,), dtype=dtype, device=codes.device)
+    out = codes.new_empty(codes.shape[:-1] + (K,), dtype=dtype)
     M.check(M.lib().moe_mx4_dequantize(cp, sp, out.numel() // K if K else 0, K, out.data_ptr(), _DTYPES[dtype],
                                        _stream(codes)))
     return out
@@ -305,7 +305,7 @@ def mx4_matmul(codes, scales, w_codes, w_scales, offsets, out=None, dtype=torch.
     if out is None:
         if dtype not in _DTYPES:
             raise ValueError(f"dtype: bf16 or fp32 is needed, got {dtype}")
-        out = torch.empty((n, N), dtype=dtype, device=codes.device)
+        out = codes.new_empty((n, N), dtype=dtype)
     op = _have(out, "out", out.dtype, (n, N), dev)
     M.check(M.lib().moe_mx4_matmul(cp, sp, n, 2 * Kh, wp, wq, E, N, fp, op, _dtype(out, "out"), _stream(codes)))
     return out
