@@ -465,10 +465,10 @@ template <typename F> cudaError_t with_width(int H, F f) {
     if (H <= 256) return f(Geom<1, 1>());
     if (H <= 512) return f(Geom<1, 2>());
     if (H <= 1024) return f(Geom<1, 4>());
-    if (H <= 2048) return f(Geom<1, 8>());
-    if (H <= 4096) return f(Geom<2, 8>());
-    if (H <= 8192) return f(Geom<4, 8>());
-    return f(Geom<8, 8>());
+    if (H <= 2048) return f(Geom<4, 2>());
+    if (H <= 4096) return f(Geom<4, 4>());
+    if (H <= 8192) return f(Geom<8, 4>());
+    return f(Geom<16, 4>());
 }
 // Few rows (fewer than warps to fill the SMs): as many warps per row as its values allow.
 template <typename F> cudaError_t with_width_few(int H, F f) {

@@ -10,15 +10,14 @@ namespace moe {
 
 // ---- rows.cu: pairs sorted by expert, rows moved there and back -----------------------------------
 constexpr int kSortThreads = 1024;       // pairs ranked at a time by one CTA of the general sort
-constexpr int kSortMaxChunks = 256;      // the pairs are split into at most about this many chunks
+constexpr int kSortMaxChunks = 148;      // the tokens are split into at most this many chunks (one CTA per SM)
 constexpr int kSmallPairs = 4096;        // up to this many pairs one launch sorts and copies
 
 struct SortArgs {
     const int* idx;
     int T, k, E;
     int n;          // T * k
-    int chunk;      // pairs per chunk of the general sort (a multiple of kSortThreads)
-    int nchunk;
+    int chunk_tokens, nchunk;   // the general sort's chunks, of whole tokens
     int* offsets;
     int* perm;
     int* pos;
@@ -28,7 +27,6 @@ struct SortArgs {
     int nvec;
 };
 
-int sort_chunk(int n);   // pairs per chunk for n pairs
 cudaError_t launch_dispatch(const SortArgs& a, int num_sms, cudaStream_t st);
 
 struct CombineArgs {

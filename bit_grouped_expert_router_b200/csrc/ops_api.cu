@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <nvtx3/nvToolsExt.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 
@@ -62,6 +63,10 @@ int current_device(int* num_sms) {
 
 constexpr int kMaxRowWidth = 65536;   // H of the moved rows
 
+// Tokens per chunk of the sort: a whole round of its CTAs where that leaves no more CTAs than SMs.
+int sort_chunk_tokens(int T, int k) { return std::max(kSortThreads / k, (T + kSortMaxChunks - 1) / kSortMaxChunks); }
+int sort_chunks(int T, int k) { return (T + sort_chunk_tokens(T, k) - 1) / sort_chunk_tokens(T, k); }
+
 int check_rows(int32_t dtype, int32_t T, int32_t k, int32_t H) {
     OPS_CHECK(dtype_ok(dtype), "unknown dtype %d", dtype);
     OPS_CHECK(T >= 0, "T must be >= 0 (got %d)", T);
@@ -112,10 +117,7 @@ int moe_ops_status(void* stream) {
 
 size_t moe_dispatch_workspace(int32_t T, int32_t k, int32_t E) {
     if (T < 0 || k < 1 || k > 32 || E < 1 || E > 256 || (long long)T * k >= (1ll << 30)) return 0;
-    const int n = T * k;
-    if (n <= kSmallPairs) return 0;
-    const int chunk = sort_chunk(n);
-    return sizeof(int) * (size_t)((n + chunk - 1) / chunk) * E;
+    return T * k <= kSmallPairs ? 0 : sizeof(int) * (size_t)sort_chunks(T, k) * E;
 }
 
 int moe_dispatch_rows(const void* x, int32_t dtype, int32_t T, int32_t H, const int32_t* idx, int32_t k, int32_t E,
@@ -140,8 +142,8 @@ int moe_dispatch_rows(const void* x, int32_t dtype, int32_t T, int32_t H, const 
     SortArgs a{};
     a.idx = idx;
     a.T = T; a.k = k; a.E = E; a.n = T * k;
-    a.chunk = sort_chunk(a.n);
-    a.nchunk = (a.n + a.chunk - 1) / a.chunk;
+    a.chunk_tokens = sort_chunk_tokens(T, k);
+    a.nchunk = sort_chunks(T, k);
     a.offsets = offsets; a.perm = perm; a.pos = pos;
     a.hist = static_cast<int*>(workspace);
     a.x = static_cast<const uint4*>(x);
@@ -269,6 +271,7 @@ int moe_mx4_quantize(const void* x, int32_t dtype, int32_t T, int32_t K, int32_t
     OPS_CHECK(dtype_ok(dtype), "unknown dtype %d", dtype);
     OPS_CHECK(T >= 0 && n_rows >= 0, "T and n_rows must be >= 0");
     OPS_CHECK(K >= 32 && K % 32 == 0 && K <= kMaxMx4Width, "K must be a multiple of 32 in [32, %d] (got %d)", kMaxMx4Width, K);
+    OPS_CHECK((long long)T * K < (1ll << 35), "T * K must be below 2^35");
     OPS_CHECK(act == MOE_ACT_NONE || act == MOE_ACT_SWIGLU, "unknown act %d", act);
     OPS_CHECK(!pos || (k >= 1 && k <= 32 && (long long)T * k < (1ll << 30)), "k must be in [1, 32] and T * k below 2^30");
     OPS_CHECK(pos || n_rows >= T, "n_rows = %d rows cannot hold T = %d", n_rows, T);

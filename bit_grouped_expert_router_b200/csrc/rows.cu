@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a) {
     const int tid = threadIdx.x;
     if (tid < a.E) cnt[tid] = 0;
     __syncthreads();
-    const int lo = blockIdx.x * a.chunk, hi = min(a.n, lo + a.chunk);
+    const int lo = blockIdx.x * a.chunk_tokens * a.k, hi = min(a.n, lo + a.chunk_tokens * a.k);
     for (int i = lo + tid; i < hi; i += kSortThreads) {
         const int e = sort_key(a.idx[i], a.E);
         if (e >= 0) atomicAdd(&cnt[e], 1);
@@ -136,8 +136,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a) {
     if (tid < a.E) a.hist[(size_t)blockIdx.x * a.E + tid] = cnt[tid];
 }
 
-// One CTA per chunk: the experts' totals and the pairs of earlier chunks from the counts of all
-// chunks, then the chunk's places in pair order, kSortThreads pairs at a time.
+// One CTA per chunk (of whole tokens): the experts' totals and the pairs of earlier chunks from the counts
+// of all chunks, then the chunk's places in pair order, up to kSortThreads pairs at a time.
 __global__ void __launch_bounds__(kSortThreads) sort_rank_kernel(SortArgs a) {
     griddep_wait();
     griddep_launch_dependents();
@@ -149,12 +149,13 @@ __global__ void __launch_bounds__(kSortThreads) sort_rank_kernel(SortArgs a) {
         const int b_lo = quarter * a.nchunk / 4, b_hi = (quarter + 1) * a.nchunk / 4;
         int sum = 0, before = 0;
         if (e < a.E) {
-            for (int b0 = b_lo; b0 < b_hi; b0 += 8) {   // eight loads in flight
-                int v[8];
+            constexpr int U = 20;   // loads in flight
+            for (int b0 = b_lo; b0 < b_hi; b0 += U) {
+                int v[U];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) v[u] = b0 + u < b_hi ? a.hist[(size_t)(b0 + u) * a.E + e] : 0;
+                for (int u = 0; u < U; ++u) v[u] = b0 + u < b_hi ? a.hist[(size_t)(b0 + u) * a.E + e] : 0;
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
+                for (int u = 0; u < U; ++u) {
                     if (b0 + u < b) before += v[u];
                     sum += v[u];
                 }
@@ -175,16 +176,16 @@ __global__ void __launch_bounds__(kSortThreads) sort_rank_kernel(SortArgs a) {
     const int kept = off[a.E];
     if (b == 0)
         for (int i = tid; i <= a.E; i += kSortThreads) a.offsets[i] = off[i];
-    const int lo = b * a.chunk, hi = min(a.n, lo + a.chunk);
-    for (int base = lo; base < hi; base += kSortThreads) {
+    const int t0 = b * a.chunk_tokens, t1 = min(a.T, t0 + a.chunk_tokens), round = kSortThreads / a.k;
+    for (int t = t0; t < t1; t += round) {
         __syncthreads();   // nxt is ready, wcnt is free
-        const int i = base + tid;
-        const int e = i < hi ? sort_key(a.idx[i], a.E) : -1;
-        const int p = rank_pairs(e, nxt, wcnt, a.E, min(kSortThreads, hi - base + 31) / 32);
-        if (i < hi) {
-            a.pos[i] = p;
-            if (p >= 0) a.perm[p] = i;
-            if (i >= kept) a.perm[i] = -1;
+        const int nt = min(round, t1 - t), pairs = nt * a.k, lo = t * a.k;
+        const int e = tid < pairs ? sort_key(a.idx[lo + tid], a.E) : -1;
+        const int p = rank_pairs(e, nxt, wcnt, a.E, (pairs + 31) / 32);
+        if (tid < pairs) {
+            a.pos[lo + tid] = p;
+            if (p >= 0) a.perm[p] = lo + tid;
+            if (lo + tid >= kept) a.perm[lo + tid] = -1;
         }
     }
 }
@@ -206,6 +207,10 @@ struct RowSplit {
     }
 };
 
+// A block's threads hold a token's row, a piece each, and store it k times.  Blocks run in token order, so
+// the rows written at a time lie close together in each expert's segment (16384 tokens of 8 x 2048 bf16:
+// 97 us, 6.2 TB/s; each SM on a range of tokens of its own, in the kernel that ranks them: 111 us with
+// these stores, 108 us with bulk copies through shared memory).
 __global__ void __launch_bounds__(256) dispatch_copy_kernel(const uint4* __restrict__ x, const int* __restrict__ pos,
                                                             int T, int k, int nvec, uint4* __restrict__ rows) {
     griddep_wait();
@@ -335,11 +340,6 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(CombineBwdArgs a) {
 }
 
 }  // namespace
-
-int sort_chunk(int n) {
-    const int per = (n + kSortMaxChunks - 1) / kSortMaxChunks;
-    return (per + kSortThreads - 1) / kSortThreads * kSortThreads;
-}
 
 cudaError_t launch_dispatch(const SortArgs& a, int num_sms, cudaStream_t st) {
     if (a.n <= kSmallPairs) {

@@ -396,7 +396,7 @@ MOE_API int moe_block_norm_backward(const void *dn, const void *dh_out, const vo
  *   act MOE_ACT_SWIGLU  v = silu(gate) * up in fp32 for x[T, 2K] = [gate | up]: the expert's activation
  * pos NULL: row t goes to row t (n_rows >= T); else to the rows pos[t, j], j < k, where pos[t, j] >= 0
  * (pos as in moe_dispatch_rows: the dispatch and the quantisation in one pass; >= n_rows: reported).
- * Other rows are left as they are.  K <= 65536. */
+ * Other rows are left as they are.  K <= 65536, T * K < 2^35. */
 #define MOE_ACT_NONE 0
 #define MOE_ACT_SWIGLU 1
 MOE_API int moe_mx4_quantize(const void *x, int32_t dtype, int32_t T, int32_t K, int32_t act, const int32_t *pos,
