@@ -1,14 +1,18 @@
-"""In-tree build of libmoe.so (the CUDA library behind include/moe.h) for sm_100a.
+"""In-tree build of libmoe.so (the CUDA library behind include/moe.h) for sm_100a, and of _torch_ops.so.
 
 Each .cu file compiles to an object in parallel; the objects link into one shared library with
 the CUDA runtime linked statically, so loading the library needs no GPU driver (symbols can be
 inspected on a machine without a GPU; the first CUDA call needs one).
+
+_torch_ops.so is the Python module behind ops.py (csrc/torch_ops.cpp: torch tensors in, libmoe calls out);
+it compiles against the installed torch and links to the libmoe.so next to it.
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
+EXT = os.path.join(PKG, "_torch_ops.so")
 SOURCES = ["api.cu", "repack.cu", "route.cu", "router_tc.cu", "gemm.cu", "decode.cu", "decode_fused.cu", "route_static.cu",
            "ops_api.cu", "rows.cu", "norm.cu", "mx4.cu"]
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
@@ -38,9 +43,9 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(EXT):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
@@ -55,6 +60,36 @@ def check_flags(flags) -> None:
     bad = [f for f in flags if f in FORBIDDEN_FLAGS]
     if bad:
         raise ValueError(f"libmoe must be built without flush-to-zero / fast math (got {bad})")
+
+
+# The system's g++, whatever $CXX names: the module must share the libstdc++ that torch has loaded (with one
+# linked in statically, its first C++ exception ends the process).
+HOST_CXX = "/usr/bin/g++" if os.path.exists("/usr/bin/g++") else "g++"
+
+
+def _compile_ext(obj: str) -> None:
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    cmd = [HOST_CXX, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", sysconfig.get_paths()["include"],
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
+           "-c", os.path.join(CSRC, "torch_ops.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"torch_ops.cpp failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _link_ext(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = EXT + ".tmp"
+    cmd = [HOST_CXX, "-shared", obj, "-o", tmp, "-L", PKG, "-l:libmoe.so", "-L", lib, "-ltorch_python",
+           "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of _torch_ops failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -76,8 +111,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stderr, file=sys.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    ext_obj = os.path.join(BUILD, "torch_ops.cpp.o")
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        ext = ex.submit(_compile_ext, ext_obj)
         objs = list(ex.map(compile_one, SOURCES))
+        ext.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-cudart", "static",
            "-Xcompiler", "-fPIC", "-o", tmp, *objs]
@@ -85,6 +123,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_ext(ext_obj)
     return LIB
 
 

@@ -531,3 +531,38 @@ def test_rows_past_32_bit_offsets():
     got = ops.dispatch_rows_backward(d.rows, d.pos)
     assert torch.equal(got[-1].float(), 8 * x[-1].float()) and torch.equal(got[T // 2].float(), 8 * x[T // 2].float())
     assert math.prod(d.rows.shape) > 1 << 31
+
+
+def test_tensors_that_do_not_fit_are_refused():
+    x, idx = torch.zeros((4, 64), device="cuda"), torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    rows, gates = torch.zeros((8, 64), device="cuda"), torch.zeros((4, 2), device="cuda")
+    codes, scales = ops.mx4_quantize(x)
+    w, ws, off = codes.view(1, 4, 32), scales.view(1, 4, 2), torch.zeros(2, dtype=torch.int32, device="cuda")
+    bad = [lambda: ops.dispatch_rows(x, idx.long(), 4), lambda: ops.dispatch_rows(x[:3], idx, 4),
+           lambda: ops.dispatch_rows(x, idx, 0), lambda: ops.dispatch_rows(x.double(), idx, 4),
+           lambda: ops.dispatch_rows(x[:, ::2], idx, 4), lambda: ops.dispatch_rows(x, idx.cpu(), 4),
+           lambda: ops.dispatch_rows(x.cpu(), idx, 4), lambda: ops.dispatch_rows(x, idx, 4, rows=rows.half()),
+           lambda: ops.dispatch_rows(None, idx, 4, rows=rows), lambda: ops.dispatch_rows(x, idx[0], 4),
+           lambda: ops.dispatch_rows_backward(rows.t(), idx), lambda: ops.combine_weighted(rows, idx, gates.half()),
+           lambda: ops.combine_weighted(rows, idx, gates[:3]), lambda: ops.combine_weighted(rows, idx, gates, base=rows),
+           lambda: ops.combine_weighted(rows, idx, gates, out=x.half()), lambda: ops.combine_weighted_backward(rows, rows, idx, gates),
+           lambda: ops.block_norm(x, x[:3]), lambda: ops.block_norm(x, x, w_pre=x), lambda: ops.block_norm(x, x, gate=x[0]),
+           lambda: ops.block_norm(x, x, out_dtype=torch.bfloat16), lambda: ops.block_norm(x.half(), x),
+           lambda: ops.block_norm(x, None, gate=x[:, 0].contiguous()), lambda: ops.block_norm(x, eps=-1.0),
+           lambda: ops.block_norm_backward(x, x, x), lambda: ops.block_norm_backward(x, x, x, r_pre=x[0]),
+           lambda: ops.block_norm_backward(None, x, x, w_pre=x[0].contiguous()),
+           lambda: ops.mx4_quantize(x[:, :40].contiguous()), lambda: ops.mx4_quantize(x, act="swiglu", pos=idx[:2]),
+           lambda: ops.mx4_quantize(x, codes=codes[:3], scales=scales[:3]), lambda: ops.mx4_dequantize(codes, scales[:, :1]),
+           lambda: ops.mx4_matmul(codes, scales, w[0], ws, off), lambda: ops.mx4_matmul(codes, scales, w, ws, off[:1]),
+           lambda: ops.mx4_matmul(codes, scales, w, ws, off, dtype=torch.float16),
+           lambda: ops.mx4_matmul(codes, scales, w[:, :3].contiguous(), ws[:, :3].contiguous(), off)]
+    for i, call in enumerate(bad):
+        with pytest.raises((ValueError, M.MoeError)):
+            call()
+            print("call", i, "was taken")
+    with pytest.raises(ValueError, match="not contiguous"):
+        ops.dispatch_rows_backward(torch.zeros((64, 64), device="cuda").t(), idx)
+    with pytest.raises(M.MoeError) as e:
+        ops.block_norm(x, eps=-1.0)
+    assert e.value.code == M.MOE_ERR_INVALID_ARG and "eps" in str(e.value)
+    assert ops.status() == M.MOE_OK

@@ -96,28 +96,40 @@ def test_workspace_sizes(lib):
     assert lib.moe_block_norm_backward_workspace(4, 12) == 0
 
 
-def test_python_calls_refuse_tensors_they_cannot_pass_on():
-    cpu = torch.zeros((2, 64))
-    for f in (ops.dispatch_rows_backward, ops.block_norm, ops.mx4_quantize):
+def test_python_calls_refuse_what_they_cannot_pass_on(lib):
+    cpu, idx = torch.zeros((2, 64)), torch.zeros((2, 2), dtype=torch.int32)
+    for call in (lambda: ops.dispatch_rows(cpu, idx, 4), lambda: ops.dispatch_rows_backward(cpu, idx),
+                 lambda: ops.combine_weighted(cpu, idx, cpu), lambda: ops.combine_weighted_backward(cpu, cpu, idx, cpu),
+                 lambda: ops.block_norm(cpu), lambda: ops.block_norm_backward(cpu, None, cpu), lambda: ops.mx4_quantize(cpu),
+                 lambda: ops.mx4_dequantize(cpu, cpu), lambda: ops.mx4_matmul(cpu, cpu, cpu, cpu, idx)):
         with pytest.raises(ValueError, match="CUDA"):
-            f(cpu)
-    with pytest.raises(ValueError, match="CUDA"):
-        ops.dispatch_rows(None, torch.zeros((2, 2), dtype=torch.int32), 4)
-    fake = lambda **kw: ops._have(cpu, "x", **{**dict(dtype=torch.float32, shape=(2, 64), device=cpu.get_device()), **kw})  # noqa: E731
-    assert fake() == cpu.data_ptr()
-    for kw in (dict(dtype=torch.bfloat16), dict(shape=(64, 2)), dict(device=0)):
-        with pytest.raises(ValueError, match="x: "):
-            fake(**kw)
-    with pytest.raises(ValueError, match="not contiguous"):
-        ops._have(cpu.t(), "x", torch.float32, (64, 2), cpu.get_device())
+            call()
+    with pytest.raises(ValueError, match="idx: a tensor"):
+        ops.dispatch_rows(cpu, None, 4)
+    with pytest.raises(ValueError, match="h_out: a tensor"):
+        ops.block_norm_backward(cpu, None, None)
+    with pytest.raises(ValueError, match="act: an integer"):
+        ops._ext().mx4_quantize(cpu, None, "four", None, None)
+    with pytest.raises(ValueError, match="act"):
+        ops.mx4_quantize(cpu, act="gelu")
+    for dtype in (torch.float64, torch.uint8):
+        with pytest.raises(ValueError, match="dtype"):
+            ops.mx4_dequantize(cpu, cpu, dtype=dtype)
+    with pytest.raises(ValueError, match="arguments"):
+        ops._ext().combine_weighted(cpu)
+
+
+def test_the_native_module_shares_the_loaded_libstdcxx(lib):
+    with open(B.EXT, "rb") as f:
+        assert b"libstdc++.so.6" in f.read()      # a needed library, not a copy inside
 
 
 def test_every_operator_takes_a_stream_and_is_documented():
     for n in ops.__all__:
         f = getattr(ops, n)
-        assert f.__doc__ or not callable(f), n
-        if inspect.isfunction(f) and n != "status":
-            assert f.__wrapped__ is not None, n
+        assert f.__doc__, n
+        if inspect.isfunction(f):
+            assert "stream" in inspect.signature(f).parameters, n
 
 
 # ---- the plain forms themselves --------------------------------------------------------------------
