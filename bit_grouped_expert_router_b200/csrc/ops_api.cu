@@ -48,10 +48,12 @@ bool null_or4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 bool dtype_ok(int d) { return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_FP16 || d == MOE_DTYPE_FP32; }
 int dtype_size(int d) { return d == MOE_DTYPE_FP32 ? 4 : 2; }
 
-// The current device: sm_100 and its SM count.
+// The current device: sm_100 and its SM count.  Its context is made current too: in a thread that has made
+// no CUDA call yet there is none, and the tensor-map encoder needs one.
 int current_device(int* num_sms) {
     int dev = 0, major = 0, minor = 0;
     cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaSetDevice(dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(num_sms, cudaDevAttrMultiProcessorCount, dev);

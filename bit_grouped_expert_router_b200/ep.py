@@ -31,6 +31,8 @@ from typing import Dict, Optional
 
 import torch
 
+from .mx4 import Mx4Experts
+
 
 @dataclass
 class DispatchPlan:
@@ -169,10 +171,41 @@ class LibraryShard:
                 L.close()
 
 
+class Mx4Shard(LibraryShard):
+    """One rank's compute steps with its experts in microscaled 4-bit floating point: the router-only handle of
+    LibraryShard, this rank's E/W routed experts and the shared expert as Mx4Experts."""
+
+    def __init__(self, router_weights: Dict[str, torch.Tensor], experts: Mx4Experts, shared: Optional[Mx4Experts],
+                 E: int, k: int, world: int, max_tokens: int = 4096, device=None, stream=None):
+        from . import _lib as M
+        if E != experts.E * world:
+            raise ValueError(f"{E} experts on {world} ranks do not leave {experts.E} on each")
+        if shared is not None and (shared.E, shared.H) != (1, experts.H):
+            raise ValueError("the shared expert must be one expert of the same hidden size")
+        self.H, self.E, self.k, self.has_shared = experts.H, E, k, shared is not None
+        self.n_local = experts.E
+        rw = {n: router_weights.get(n) for n in ("router", "router_bias", "shared_gate")}
+        self.router = M.Layer(rw, self.H, experts.I, E, k, self.has_shared, max_tokens=max_tokens, decode_max_tokens=0,
+                              flags=M.MOE_FLAG_NO_EXPERTS, device=device, stream=stream)
+        self.experts, self.shared = experts, shared
+
+    def experts_forward(self, rows, ids, gates):
+        return self.experts.forward(rows, ids.view(-1, 1), gates.view(-1, 1))
+
+    def shared_forward(self, x, shared_gate):
+        if self.shared is None:
+            return None
+        ids = torch.zeros((x.shape[0], 1), dtype=torch.int32, device=x.device)
+        return self.shared.forward(x, ids, shared_gate.view(-1, 1).contiguous())
+
+    def close(self):
+        self.router.close()
+
+
 class ExpertParallelLayer:
     """One MoE layer with its routed experts sharded over ``exchange.world`` ranks.
 
-    ``shard`` runs the compute steps on this rank (``LibraryShard``: libmoe on the rank's GPU);
+    ``shard`` runs the compute steps on this rank (``LibraryShard`` or ``Mx4Shard``: libmoe on the rank's GPU);
     ``exchange`` moves rows between ranks.  Every rank calls ``forward`` on its own tokens, in the same
     order as the other ranks (the exchanges are collective)."""
 

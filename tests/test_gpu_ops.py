@@ -1,6 +1,7 @@
 """The operators around the experts against their plain 64-bit forms (tests/ops_plain.py): rows sorted by
 expert and back, block norms, microscaled 4-bit floating point, and a run of them together."""
 import math
+import threading
 
 import pytest
 import torch
@@ -468,6 +469,26 @@ def test_equal_calls_give_equal_bits_on_any_stream():
     for o in outs[1:]:
         for p, q in zip(outs[0], o):
             assert torch.equal(p, q)
+
+
+def test_calls_from_threads_of_their_own():
+    """A thread whose first CUDA call is the operator, and several at once on streams of their own."""
+    a = [t.cuda() for t in matmul_inputs([70, 30], 128, 256, seed=5)]
+    want = ops.mx4_matmul(*a)
+    outs = [torch.zeros_like(want) for _ in range(4)]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=lambda i=i: [ops.mx4_matmul(*a, out=outs[i], stream=streams[i]) for _ in range(5)])
+               for i in range(4)]
+    one = threading.Thread(target=lambda: ops._ext().mx4_matmul(*a, outs[0], M.MOE_DTYPE_BF16))
+    one.start()
+    one.join()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want)
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs) and ops.status() == M.MOE_OK
 
 
 def test_captured_in_a_graph_and_replayed_on_new_inputs():
