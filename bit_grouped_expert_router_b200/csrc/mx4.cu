@@ -181,25 +181,35 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t* __r
 // operand and the rows the N operand, so a short segment costs a narrow instruction (N = 16 and up)
 // instead of a padded one.  A persistent CTA walks units; per step of 256 columns
 //   warp 0       TMA: the 128 x 128-byte weight tile and the row tile (boxes of 32 rows), 128-byte swizzle
-//   warps 8-11   the scales: a thread loads those of its rows 32 bytes at a time, ahead of their use, and writes
-//                each step's eight in the order tcgen05.cp wants (512 bytes per 128 rows and 128
-//                columns: row r at 16 (r % 32) + 4 (r / 32))
+//   warps 8-11   the scales: a thread loads those of its rows 32 bytes at a time (four steps), ahead of their use,
+//                and writes them in the order tcgen05.cp wants (512 bytes per 128 rows and 128 columns:
+//                row r at 16 (r % 32) + 4 (r / 32)), to a ring of their own
 //   warp 1       tcgen05.cp of the scales to tensor memory, then four MMAs of 64 columns
 //   warps 4-7, 12-15  epilogue of the unit before: tensor memory -> shared memory -> row stores
 // Tensor memory: two accumulators of 224 columns (the epilogue of one overlaps the MMAs of the next) and
 // 2 x 32 columns of scales, alternating by step.
+//
+// What bounds it: weights and results from and to HBM while the rows are few (results alone pass at the rate
+// of a fill, 3.9 TB/s), then the traffic from L2 (weights once per row tile, rows once per feature tile: 66 us
+// of 85 for 32768 x 1024 x 2048 with nothing but the loads, 9.9 TB/s), and, run after run, the power cap (1.65 GHz
+// there).  Pairs of CTAs on one tile of 256 features (cta_group::2), which read the rows half as often, gained
+// 3 to 5% from 131072 rows on and lost 1 to 30% below: their barriers and commits cross CTAs every step.
 constexpr int kTM = 128;             // features per unit
 constexpr int kTN = 224;             // most rows per unit
 constexpr int kStep = 256;           // columns per step: 128 bytes of codes per row
 constexpr int kRing = 4;
 constexpr int kABytes = kTM * 128;
 constexpr int kBBytes = kTN * 128;
-constexpr int kSfBytes = 2 * (512 + 2 * 512);   // per 128 columns: 512 B of weight scales, 2 x 512 B of row scales
-constexpr int kStageBytes = kABytes + kBBytes + kSfBytes;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kSfSteps = 4;          // steps whose scales come together: a 32-byte sector of every row
+constexpr int kSfRing = 2;
+constexpr int kSfBytes = 2 * (512 + 2 * 512);   // per step: 512 B of weight scales, 2 x 512 B of row scales, twice
 constexpr int kThreadsMm = 512;
 constexpr int kTmemSf = 448;         // first tensor-memory column of the scales
 constexpr int kOutPitch = kTM * 2 + 16, kOutBytes = 32 * kOutPitch;   // a bf16 chunk of the epilogue
-constexpr int kSmemMm = 1024 + kRing * kStageBytes + 4 * kOutBytes;
+constexpr int kSfAt = kRing * kStageBytes, kOutAt = kSfAt + kSfRing * kSfSteps * kSfBytes;
+constexpr int kSmemMm = 1024 + kOutAt + 2 * kOutBytes;
+static_assert(kStageBytes % 1024 == 0, "stages keep the swizzle's alignment");
 
 struct Unit {
     int e, mt, row0, rows;   // expert, feature tile, first row, rows (1..224)
@@ -322,20 +332,24 @@ template <typename T>
 __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs a, const __grid_constant__ CUtensorMap tm_w,
                                                                    const __grid_constant__ CUtensorMap tm_x) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full[kRing], empty[kRing], dfull[2], dempty[2], drain;
+    __shared__ __align__(8) uint64_t full[kRing], empty[kRing], sffull[kSfRing], sfempty[kSfRing], dfull[2], dempty[2], drain;
     __shared__ int ustart[257], seg[256], len[256], wsum[8];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_word;
     uint8_t* ring = smem_raw + (1024u - (smem_u32(smem_raw) & 1023u) & 1023u);
-    uint8_t* out = ring + kRing * kStageBytes;
+    uint8_t* out = ring + kOutAt;
     volatile int* abort_flag = &abort_word;
     uint32_t* status = g_ops_status;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = lane_id();
 
     if (tid == 0) {
         for (int i = 0; i < kRing; ++i) {
-            mbar_init(&full[i], 5);    // the TMA thread and the four scale warps
+            mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < kSfRing; ++i) {
+            mbar_init(&sffull[i], 4);    // the scale warps
+            mbar_init(&sfempty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&dfull[i], 1);
@@ -405,14 +419,13 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
             }
         }
     producer_done:
-        // every copy issued must land before the CTA may exit (bounded: after an abort the scale
-        // warps may have left without their arrivals)
+        // every copy issued must land before the CTA may exit
         for (uint32_t i = it > (uint32_t)kRing ? it - kRing : 0u; i < it; ++i)
             mbar_drain(&full[i % kRing], (i / kRing) & 1u);
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issuer
         const uint32_t lead = elect_lane();
-        uint32_t it = 0, tl = 0;
+        uint32_t it = 0, sfi = 0, tl = 0;
         bool issued = false;
         for (int u = blockIdx.x; u < total; u += gridDim.x, ++tl) {
             const Unit un = find_unit(u, ustart, seg, len, a.E, MT, true);
@@ -424,11 +437,16 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
             const uint32_t d = tmem + ab * kTN;
             const uint32_t i0 = idesc_mx4(n, 0), i2 = idesc_mx4(n, 2);
             for (int ks = 0; ks < KS; ++ks, ++it) {
-                const int s = it % kRing;
+                const int s = it % kRing, j = ks % kSfSteps, c4 = sfi % kSfRing;
+                if (j == 0) {
+                    ok = mbar_wait(&sffull[c4], (sfi / kSfRing) & 1u, abort_flag, status);
+                    if (!__all_sync(0xffffffffu, ok)) goto mma_done;
+                }
                 ok = mbar_wait(&full[s], (it / kRing) & 1u, abort_flag, status);
                 if (!__all_sync(0xffffffffu, ok)) goto mma_done;
                 tc_fence_after();
-                const uint32_t st = smem_u32(ring) + s * kStageBytes, sf = st + kABytes + kBBytes;
+                const uint32_t st = smem_u32(ring) + s * kStageBytes;
+                const uint32_t sf = smem_u32(ring) + kSfAt + (c4 * kSfSteps + j) * kSfBytes;
                 const uint32_t tsf = tmem + kTmemSf + (it & 1u) * 32;
                 const int kmma = min(4, (a.K - ks * kStep + 63) / 64);
                 for (int c = 0; c < (kmma + 1) / 2; ++c) {
@@ -444,6 +462,10 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
                                 tsf + 8 + (kk >> 1) * 8, (ks | kk) != 0 ? 1u : 0u, lead);
                 issued = true;
                 commit_lead(&empty[s], lead);
+                if (j == kSfSteps - 1 || ks == KS - 1) {
+                    commit_lead(&sfempty[c4], lead);
+                    ++sfi;
+                }
             }
             commit_lead(&dfull[ab], lead);
         }
@@ -471,7 +493,7 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
             }
         };
         const uint32_t at = (uint32_t)((r & 31) * 16 + (r >> 5) * 4);
-        uint32_t it = 0;
+        uint32_t sfi = 0;
         int steps = 0;   // of the sector at hand (none yet)
         bool more = u < total;
         if (more) un = find_unit(u, ustart, seg, len, a.E, MT);
@@ -485,8 +507,8 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
             steps = 0;
             if (more) {
                 fetch();
-                steps = min(4, KS - ks0);
-                ks0 += 4;
+                steps = min(kSfSteps, KS - ks0);
+                ks0 += kSfSteps;
                 if (ks0 >= KS) {
                     ks0 = 0;
                     u += gridDim.x;
@@ -494,24 +516,25 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
                     if (more) un = find_unit(u, ustart, seg, len, a.E, MT);
                 }
             }
+            if (now == 0) continue;
+            const int c = sfi % kSfRing;
+            const bool ok = mbar_wait(&sfempty[c], ((sfi / kSfRing) & 1u) ^ 1u, abort_flag, status);
+            if (!__all_sync(0xffffffffu, ok)) goto scales_done;
+            uint8_t* sf = ring + kSfAt + c * kSfSteps * kSfBytes + at;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kSfSteps; ++j) {
                 if (j >= now) break;
-                const int s = it % kRing;
-                const bool ok = mbar_wait(&empty[s], ((it / kRing) & 1u) ^ 1u, abort_flag, status);
-                if (!__all_sync(0xffffffffu, ok)) goto scales_done;
-                uint8_t* sf = ring + s * kStageBytes + kABytes + kBBytes + at;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    *reinterpret_cast<uint32_t*>(sf + c * 512) = cur[0][2 * j + c];
-                    *reinterpret_cast<uint32_t*>(sf + 1024 + c * 1024) = cur[1][2 * j + c];
-                    *reinterpret_cast<uint32_t*>(sf + 1536 + c * 1024) = cur[2][2 * j + c];
+                for (int h = 0; h < 2; ++h) {
+                    *reinterpret_cast<uint32_t*>(sf + j * kSfBytes + h * 512) = cur[0][2 * j + h];
+                    *reinterpret_cast<uint32_t*>(sf + j * kSfBytes + 1024 + h * 1024) = cur[1][2 * j + h];
+                    *reinterpret_cast<uint32_t*>(sf + j * kSfBytes + 1536 + h * 1024) = cur[2][2 * j + h];
                 }
-                fence_proxy_async_smem();   // generic-proxy stores -> visible to tcgen05.cp
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[s]);
-                ++it;
             }
+            fence_proxy_async_smem();   // generic-proxy stores -> visible to tcgen05.cp
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sffull[c]);
+            ++sfi;
         }
     scales_done:;
     } else if (warp >= 4) {
@@ -524,7 +547,6 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
         // directly, 64 bytes a row: 162 us for 32768 x 2048 outputs of 512 columns, 108 us this way.)
         const int q = warp & 3, grp = warp >= 12 ? 1 : 0, gt = tid & 127;
         uint32_t tl = 0;
-        int buf = 0;
         for (int u = blockIdx.x; u < total; u += gridDim.x, ++tl) {
             const Unit un = find_unit(u, ustart, seg, len, a.E, MT);
             const uint32_t ab = tl & 1u;
@@ -543,9 +565,8 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
                         if (c0 + r < un.rows && f < a.N) y[(size_t)(c0 + r) * a.N + f] = __uint_as_float(v[r]);
                 } else {
                     const bool odd = lane & 1;
-                    uint8_t* st = out + (grp * 2 + buf) * kOutBytes;
+                    uint8_t* st = out + grp * kOutBytes;
                     uint8_t* at = st + (odd ? 4 * kOutPitch : 0) + (32 * q + (lane & ~1)) * 2;
-                    buf ^= 1;
 #pragma unroll
                     for (int r8 = 0; r8 < 32; r8 += 8)
 #pragma unroll
@@ -554,13 +575,16 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
                             const float lo = __uint_as_float(odd ? got : v[r]), hi = __uint_as_float(odd ? v[r + 4] : got);
                             *reinterpret_cast<__nv_bfloat162*>(at + r * kOutPitch) = __floats2bfloat162_rn(lo, hi);
                         }
-                    named_bar(3 + grp, 128);   // (who writes a buffer again has passed the barrier behind its readers)
+                    named_bar(3 + grp, 128);
+                    uint4 o[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        o[i] = *reinterpret_cast<const uint4*>(st + (i * 8 + (gt >> 4)) * kOutPitch + (gt & 15) * 16);
+                    named_bar(3 + grp, 128);   // read: the next chunk may have the buffer
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int r = i * 8 + (gt >> 4), c = (gt & 15) * 8;
-                        if (c0 + r < un.rows && f0 + c < a.N)
-                            *reinterpret_cast<uint4*>(y + (size_t)(c0 + r) * a.N + f0 + c) =
-                                *reinterpret_cast<const uint4*>(st + r * kOutPitch + c * 2);
+                        const int r = c0 + i * 8 + (gt >> 4), c = (gt & 15) * 8;
+                        if (r < un.rows && f0 + c < a.N) *reinterpret_cast<uint4*>(y + (size_t)r * a.N + f0 + c) = o[i];
                     }
                 }
             }

@@ -112,7 +112,6 @@ cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, l
 
 struct Mx4MatmulArgs {
     const uint8_t* scales;
-    const uint8_t* w_codes;
     const uint8_t* w_scales;
     const int* offsets;
     void* y;

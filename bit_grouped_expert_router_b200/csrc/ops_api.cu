@@ -318,7 +318,7 @@ int moe_mx4_matmul(const uint8_t* codes, const uint8_t* scales, int32_t n_rows, 
     int rc = encode_codes_map(&tm_w, w_codes, (long long)E * N, K / 2, 128);
     if (rc == MOE_OK) rc = encode_codes_map(&tm_x, codes, n_rows, K / 2, kMx4BoxRows);
     if (rc != MOE_OK) return rc;
-    const Mx4MatmulArgs a{scales, w_codes, w_scales, offsets, y, n_rows, K, N, E};
+    const Mx4MatmulArgs a{scales, w_scales, offsets, y, n_rows, K, N, E};
     return launched("moe_mx4_matmul", launch_mx4_matmul(a, tm_w, tm_x, dtype, sms, static_cast<cudaStream_t>(stream)));
 }
 
