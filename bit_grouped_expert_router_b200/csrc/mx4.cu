@@ -195,28 +195,32 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t* __r
 // there).  Pairs of CTAs on one tile of 256 features (cta_group::2), which read the rows half as often, gained
 // 3 to 5% from 131072 rows on and lost 1 to 30% below: their barriers and commits cross CTAs every step.
 constexpr int kTM = 128;             // features per unit
-constexpr int kTN = 224;             // most rows per unit
 constexpr int kStep = 256;           // columns per step: 128 bytes of codes per row
-constexpr int kRing = 4;
-constexpr int kABytes = kTM * 128;
-constexpr int kBBytes = kTN * 128;
-constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kSfSteps = 4;          // steps whose scales come together: a 32-byte sector of every row
 constexpr int kSfRing = 2;
 constexpr int kSfBytes = 2 * (512 + 2 * 512);   // per step: 512 B of weight scales, 2 x 512 B of row scales, twice
 constexpr int kThreadsMm = 512;
 constexpr int kTmemSf = 448;         // first tensor-memory column of the scales
 constexpr int kOutPitch = kTM * 2 + 16, kOutBytes = 32 * kOutPitch;   // a bf16 chunk of the epilogue
-constexpr int kSfAt = kRing * kStageBytes, kOutAt = kSfAt + kSfRing * kSfSteps * kSfBytes;
-constexpr int kSmemMm = 1024 + kOutAt + 2 * kOutBytes;
-static_assert(kStageBytes % 1024 == 0, "stages keep the swizzle's alignment");
+
+// TN: most rows per unit.  224 where experts have many rows; with 64 the ring has seven stages instead of four,
+// and more of the weights are in flight where they are all there is to load (see launch_mx4_matmul).
+template <int TN> struct MmCfg {
+    static constexpr int kRing = TN > 64 ? 4 : 7;
+    static constexpr int kABytes = kTM * 128, kBBytes = TN * 128, kStageBytes = kABytes + kBBytes;
+    static constexpr int kSfAt = kRing * kStageBytes, kOutAt = kSfAt + kSfRing * kSfSteps * kSfBytes;
+    static constexpr int kSmem = 1024 + kOutAt + 2 * kOutBytes;
+    static_assert(kStageBytes % 1024 == 0, "stages keep the swizzle's alignment");
+    static_assert(2 * TN <= kTmemSf, "two accumulators in front of the scales");
+};
 
 struct Unit {
-    int e, mt, row0, rows;   // expert, feature tile, first row, rows (1..224)
+    int e, mt, row0, rows;   // expert, feature tile, first row, rows (1..TN)
 };
 
 // Unit u of the list (experts in order, row tiles within an expert, feature tiles within a row tile):
 // a segment's 16-row groups are dealt evenly over its tiles.
+template <int TN>
 __device__ __forceinline__ Unit find_unit(int u, const int* ustart, const int* seg, const int* len, int E, int MT,
                                           bool whole_warp = false) {
     int lo = 0, hi = E;   // ustart[lo] <= u < ustart[hi]
@@ -225,7 +229,7 @@ __device__ __forceinline__ Unit find_unit(int u, const int* ustart, const int* s
         if (ustart[mid] <= u) lo = mid;
         else hi = mid;
     }
-    const int n = len[lo], groups = (n + 15) / 16, tiles = (n + kTN - 1) / kTN;
+    const int n = len[lo], groups = (n + 15) / 16, tiles = (n + TN - 1) / TN;
     const int v = u - ustart[lo], tile = v / MT;
     const int each = groups / tiles, left = groups - each * tiles;   // the first `left` tiles have one group more
     const int g0 = each * tile + min(tile, left), g1 = g0 + each + (tile < left ? 1 : 0);
@@ -328,16 +332,18 @@ __device__ __forceinline__ void load_scales(uint32_t (&v)[8], const uint8_t* row
     }
 }
 
-template <typename T>
+template <typename T, int TN>
 __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs a, const __grid_constant__ CUtensorMap tm_w,
                                                                    const __grid_constant__ CUtensorMap tm_x) {
+    using C = MmCfg<TN>;
+    constexpr int kRing = C::kRing;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[kRing], empty[kRing], sffull[kSfRing], sfempty[kSfRing], dfull[2], dempty[2], drain;
     __shared__ int ustart[257], seg[256], len[256], wsum[8];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_word;
     uint8_t* ring = smem_raw + (1024u - (smem_u32(smem_raw) & 1023u) & 1023u);
-    uint8_t* out = ring + kOutAt;
+    uint8_t* out = ring + C::kOutAt;
     volatile int* abort_flag = &abort_word;
     uint32_t* status = g_ops_status;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = lane_id();
@@ -377,7 +383,7 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
             if (blockIdx.x == 0 && (s0 != o0 || s1 != o1)) set_status(status, MOE_STATUS_BOUNDS);
             seg[tid] = s0;
             len[tid] = s1 - s0;
-            mine = (s1 - s0 + kTN - 1) / kTN * MT;
+            mine = (s1 - s0 + TN - 1) / TN * MT;
         }
         inc = mine;
 #pragma unroll
@@ -405,17 +411,17 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
         const uint32_t lead = elect_lane();
         uint32_t it = 0;
         for (int u = blockIdx.x; u < total; u += gridDim.x) {
-            const Unit un = find_unit(u, ustart, seg, len, a.E, MT, true);
+            const Unit un = find_unit<TN>(u, ustart, seg, len, a.E, MT, true);
             const int boxes = (un.rows + kMx4BoxRows - 1) / kMx4BoxRows, wrow = un.e * a.N + un.mt * kTM;
             for (int ks = 0; ks < KS; ++ks, ++it) {
                 const int s = it % kRing;
                 const bool ok = mbar_wait(&empty[s], ((it / kRing) & 1u) ^ 1u, abort_flag, status);
                 if (!__all_sync(0xffffffffu, ok)) goto producer_done;
-                const uint32_t st = smem_u32(ring) + s * kStageBytes;
-                expect_lead(&full[s], kABytes + boxes * kMx4BoxRows * 128, lead);
+                const uint32_t st = smem_u32(ring) + s * C::kStageBytes;
+                expect_lead(&full[s], C::kABytes + boxes * kMx4BoxRows * 128, lead);
                 tma_lead(st, &tm_w, ks * 128, wrow, &full[s], lead);
                 for (int b = 0; b < boxes; ++b)
-                    tma_lead(st + kABytes + b * kMx4BoxRows * 128, &tm_x, ks * 128, un.row0 + b * kMx4BoxRows, &full[s], lead);
+                    tma_lead(st + C::kABytes + b * kMx4BoxRows * 128, &tm_x, ks * 128, un.row0 + b * kMx4BoxRows, &full[s], lead);
             }
         }
     producer_done:
@@ -428,13 +434,13 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
         uint32_t it = 0, sfi = 0, tl = 0;
         bool issued = false;
         for (int u = blockIdx.x; u < total; u += gridDim.x, ++tl) {
-            const Unit un = find_unit(u, ustart, seg, len, a.E, MT, true);
+            const Unit un = find_unit<TN>(u, ustart, seg, len, a.E, MT, true);
             const int n = (un.rows + 15) / 16 * 16;
             const uint32_t ab = tl & 1u;
             bool ok = mbar_wait(&dempty[ab], ((tl >> 1) & 1u) ^ 1u, abort_flag, status);
             if (!__all_sync(0xffffffffu, ok)) goto mma_done;
             tc_fence_after();
-            const uint32_t d = tmem + ab * kTN;
+            const uint32_t d = tmem + ab * TN;
             const uint32_t i0 = idesc_mx4(n, 0), i2 = idesc_mx4(n, 2);
             for (int ks = 0; ks < KS; ++ks, ++it) {
                 const int s = it % kRing, j = ks % kSfSteps, c4 = sfi % kSfRing;
@@ -445,16 +451,16 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
                 ok = mbar_wait(&full[s], (it / kRing) & 1u, abort_flag, status);
                 if (!__all_sync(0xffffffffu, ok)) goto mma_done;
                 tc_fence_after();
-                const uint32_t st = smem_u32(ring) + s * kStageBytes;
-                const uint32_t sf = smem_u32(ring) + kSfAt + (c4 * kSfSteps + j) * kSfBytes;
+                const uint32_t st = smem_u32(ring) + s * C::kStageBytes;
+                const uint32_t sf = smem_u32(ring) + C::kSfAt + (c4 * kSfSteps + j) * kSfBytes;
                 const uint32_t tsf = tmem + kTmemSf + (it & 1u) * 32;
                 const int kmma = min(4, (a.K - ks * kStep + 63) / 64);
                 for (int c = 0; c < (kmma + 1) / 2; ++c) {
                     tmem_cp_scales(tsf + c * 4, scale_desc(sf + c * 512), lead);
                     tmem_cp_scales(tsf + 8 + c * 8, scale_desc(sf + 1024 + c * 1024), lead);
-                    if (n > 128) tmem_cp_scales(tsf + 12 + c * 8, scale_desc(sf + 1024 + c * 1024 + 512), lead);
+                    if (TN > 128 && n > 128) tmem_cp_scales(tsf + 12 + c * 8, scale_desc(sf + 1024 + c * 1024 + 512), lead);
                 }
-                const uint64_t ad = sdesc_sw128(st), bd = sdesc_sw128(st + kABytes);
+                const uint64_t ad = sdesc_sw128(st), bd = sdesc_sw128(st + C::kABytes);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     if (kk < kmma)
@@ -487,7 +493,7 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
             const int f = un.mt * kTM + r;
             load_scales(nxt[0], a.w_scales + ((size_t)un.e * a.N + f) * nk, ks0 * 8, f < a.N ? nk : 0, align);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < (TN > 128 ? 2 : 1); ++i) {
                 const int row = r + 128 * i;
                 load_scales(nxt[1 + i], a.scales + (size_t)(un.row0 + row) * nk, ks0 * 8, row < un.rows ? nk : 0, align);
             }
@@ -496,7 +502,7 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
         uint32_t sfi = 0;
         int steps = 0;   // of the sector at hand (none yet)
         bool more = u < total;
-        if (more) un = find_unit(u, ustart, seg, len, a.E, MT);
+        if (more) un = find_unit<TN>(u, ustart, seg, len, a.E, MT);
         while (more || steps > 0) {
             uint32_t cur[3][8];
             const int now = steps;
@@ -513,14 +519,14 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
                     ks0 = 0;
                     u += gridDim.x;
                     more = u < total;
-                    if (more) un = find_unit(u, ustart, seg, len, a.E, MT);
+                    if (more) un = find_unit<TN>(u, ustart, seg, len, a.E, MT);
                 }
             }
             if (now == 0) continue;
             const int c = sfi % kSfRing;
             const bool ok = mbar_wait(&sfempty[c], ((sfi / kSfRing) & 1u) ^ 1u, abort_flag, status);
             if (!__all_sync(0xffffffffu, ok)) goto scales_done;
-            uint8_t* sf = ring + kSfAt + c * kSfSteps * kSfBytes + at;
+            uint8_t* sf = ring + C::kSfAt + c * kSfSteps * kSfBytes + at;
 #pragma unroll
             for (int j = 0; j < kSfSteps; ++j) {
                 if (j >= now) break;
@@ -528,7 +534,7 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
                 for (int h = 0; h < 2; ++h) {
                     *reinterpret_cast<uint32_t*>(sf + j * kSfBytes + h * 512) = cur[0][2 * j + h];
                     *reinterpret_cast<uint32_t*>(sf + j * kSfBytes + 1024 + h * 1024) = cur[1][2 * j + h];
-                    *reinterpret_cast<uint32_t*>(sf + j * kSfBytes + 1536 + h * 1024) = cur[2][2 * j + h];
+                    if (TN > 128) *reinterpret_cast<uint32_t*>(sf + j * kSfBytes + 1536 + h * 1024) = cur[2][2 * j + h];
                 }
             }
             fence_proxy_async_smem();   // generic-proxy stores -> visible to tcgen05.cp
@@ -548,12 +554,12 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
         const int q = warp & 3, grp = warp >= 12 ? 1 : 0, gt = tid & 127;
         uint32_t tl = 0;
         for (int u = blockIdx.x; u < total; u += gridDim.x, ++tl) {
-            const Unit un = find_unit(u, ustart, seg, len, a.E, MT);
+            const Unit un = find_unit<TN>(u, ustart, seg, len, a.E, MT);
             const uint32_t ab = tl & 1u;
             const bool ok = mbar_wait(&dfull[ab], (tl >> 1) & 1u, abort_flag, status);
             if (named_bar_or(1 + grp, 128, !ok)) break;   // the group leaves together
             tc_fence_after();
-            const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + ab * kTN;
+            const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + ab * TN;
             const int f0 = un.mt * kTM, f = f0 + 32 * q + lane;
             T* y = static_cast<T*>(a.y) + (size_t)un.row0 * a.N;
             for (int c0 = 32 * grp; c0 < un.rows; c0 += 64) {
@@ -625,23 +631,30 @@ cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, l
     });
 }
 
-template <typename T>
+template <typename T, int TN>
 static cudaError_t launch_matmul(const Mx4MatmulArgs& a, const CUtensorMap& tm_w, const CUtensorMap& tm_x, int num_sms,
                                  cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(mx4_matmul_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kSmemMm);
+    const cudaError_t e = cudaFuncSetAttribute(mx4_matmul_kernel<T, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               MmCfg<TN>::kSmem);
     if (e != cudaSuccess) return e;
-    // at most one row tile per kTN rows and one more per expert that has rows
-    const long long tiles = (long long)a.R / kTN + (a.E < a.R ? a.E : a.R);
+    // at most one row tile per TN rows and one more per expert that has rows
+    const long long tiles = (long long)a.R / TN + (a.E < a.R ? a.E : a.R);
     const long long units = tiles * ((a.N + kTM - 1) / kTM);
-    return launch_pdl(mx4_matmul_kernel<T>, dim3((unsigned)(units < num_sms ? units : num_sms)), dim3(kThreadsMm),
-                      kSmemMm, st, a, tm_w, tm_x);
+    return launch_pdl(mx4_matmul_kernel<T, TN>, dim3((unsigned)(units < num_sms ? units : num_sms)), dim3(kThreadsMm),
+                      MmCfg<TN>::kSmem, st, a, tm_w, tm_x);
 }
 
 cudaError_t launch_mx4_matmul(const Mx4MatmulArgs& a, const CUtensorMap& tm_w, const CUtensorMap& tm_x, int dtype,
                               int num_sms, cudaStream_t st) {
-    if (dtype == MOE_DTYPE_BF16) return launch_matmul<__nv_bfloat16>(a, tm_w, tm_x, num_sms, st);
-    if (dtype == MOE_DTYPE_FP32) return launch_matmul<float>(a, tm_w, tm_x, num_sms, st);
+    // Row tiles of 64 up to 32 rows per expert on average: 256 experts of 1024 x 2048 with 1 to 32 rows each 45 to 56 us
+    // with them, 49 to 60 us with 224; with 64 rows each 85 and 71 us.
+    const bool few = a.R <= 32ll * a.E;
+    if (dtype == MOE_DTYPE_BF16)
+        return few ? launch_matmul<__nv_bfloat16, 64>(a, tm_w, tm_x, num_sms, st)
+                   : launch_matmul<__nv_bfloat16, 224>(a, tm_w, tm_x, num_sms, st);
+    if (dtype == MOE_DTYPE_FP32)
+        return few ? launch_matmul<float, 64>(a, tm_w, tm_x, num_sms, st)
+                   : launch_matmul<float, 224>(a, tm_w, tm_x, num_sms, st);
     return cudaErrorInvalidValue;
 }
 

@@ -362,11 +362,11 @@ def test_swiglu_quantize(R, K, dtype):
     assert ((got - v.view(R, -1, 32)).abs() <= unit * (gap + m * d)).all()
 
 
-# one row; segments on both sides of a row tile (224) and of the 16-row groups; empty experts; features
-# that end inside a tile; columns that end inside a step (256), an MMA (64) and a scale word
+# one row; segments on both sides of a row tile (224, or 64 where experts average 32 rows or fewer) and of the
+# 16-row groups; empty experts; features that end inside a tile; columns that end inside a step (256), an MMA (64) and a scale word
 MATMUL = [([1], 8, 32), ([1], 128, 256), ([0, 3, 0, 17], 136, 64), ([224, 225, 0, 16], 256, 512), ([449, 1, 31], 264, 288),
           ([128, 129, 300], 1024, 2048), ([5] * 40, 128, 96), ([700], 72, 1056), ([33, 0, 0, 0], 512, 4128),
-          ([2] * 256, 24, 128)]
+          ([2] * 256, 24, 128), ([300] + [0] * 30 + [65], 264, 2080), ([64, 1, 0, 63] + [0] * 20, 128, 5120)]
 
 
 def matmul_inputs(counts, N, K, extra=0, seed=0):
