@@ -373,17 +373,30 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
     }
     griddep_wait();
     griddep_launch_dependents();
-    // the unit list: segments held to [0, R], row tiles per expert, first unit of each expert
+    // the unit list: row tiles per expert, first unit of each.  Expert e's segment runs from the largest of
+    // offsets[0..e] to the largest of offsets[0..e+1], held to [0, R]: the offsets themselves if they are sound,
+    // and disjoint segments whatever they are.
     const int MT = (a.N + kTM - 1) / kTM;
-    int mine = 0, inc = 0;
+    int mine = 0, inc = 0, low = 0, high = 0;
     if (tid < 256) {
+        low = tid < a.E ? min(max(a.offsets[tid], 0), a.R) : 0;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, low, off);
+            if (lane >= off) low = max(low, o);
+        }
+        if (lane == 31) wsum[warp] = low;
+    }
+    __syncthreads();
+    if (tid < 256) {
+        for (int w = 0; w < warp; ++w) low = max(low, wsum[w]);
         if (tid < a.E) {
-            const int o0 = a.offsets[tid], o1 = a.offsets[tid + 1];
-            const int s0 = min(max(o0, 0), a.R), s1 = min(max(o1, s0), a.R);
-            if (blockIdx.x == 0 && (s0 != o0 || s1 != o1)) set_status(status, MOE_STATUS_BOUNDS);
-            seg[tid] = s0;
-            len[tid] = s1 - s0;
-            mine = (s1 - s0 + TN - 1) / TN * MT;
+            const int next = a.offsets[tid + 1];
+            high = max(low, min(next, a.R));
+            if (blockIdx.x == 0 && (low != a.offsets[tid] || high != next)) set_status(status, MOE_STATUS_BOUNDS);
+            seg[tid] = low;
+            len[tid] = high - low;
+            mine = (high - low + TN - 1) / TN * MT;
         }
         inc = mine;
 #pragma unroll
@@ -391,8 +404,9 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
             const int o = __shfl_up_sync(0xffffffffu, inc, off);
             if (lane >= off) inc += o;
         }
-        if (lane == 31) wsum[warp] = inc;
     }
+    __syncthreads();   // (wsum is read)
+    if (tid < 256 && lane == 31) wsum[warp] = inc;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -62,10 +62,15 @@ __device__ __forceinline__ int rank_pairs(int e, int* nxt, int* wcnt, int E, int
     __syncthreads();
     for (int i = tid; i < E; i += blockDim.x) {
         int run = nxt[i];
-        for (int w = 0; w < nwarps; ++w) {
-            const int v = wcnt[w * E + i];
-            wcnt[w * E + i] = run;
-            run += v;
+        for (int w0 = 0; w0 < nwarps; w0 += 8) {   // eight loads before their stores
+            int v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = w0 + u < nwarps ? wcnt[(w0 + u) * E + i] : 0;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (w0 + u < nwarps) wcnt[(w0 + u) * E + i] = run;
+                run += v[u];
+            }
         }
         nxt[i] = run;
     }

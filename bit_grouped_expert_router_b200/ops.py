@@ -8,6 +8,8 @@ Argument marshalling only, like ``_lib`` (the tensors are checked and passed on 
 one device, run there on ``stream`` (default: that device's current stream) without synchronising, and allocate
 what they return, and their scratch, on that stream unless an output tensor is given.  A wrong tensor raises
 ValueError, a refusal by the library MoeError; what the kernels find on the device is kept for ``status``.
+Tensors passed with ``stream`` must be ready there and stay alive until the stream has passed the call.  No graph of
+automatic differentiation is recorded: the gradients are functions of their own.
 There is no fallback: if the module has not been built, the first call fails loudly.
 """
 from __future__ import annotations

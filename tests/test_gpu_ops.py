@@ -1,6 +1,9 @@
 """The operators around the experts against their plain 64-bit forms (tests/ops_plain.py): rows sorted by
 expert and back, block norms, microscaled 4-bit floating point, and a run of them together."""
 import math
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -444,8 +447,23 @@ def test_matmul_holds_bad_offsets_to_the_rows_and_reports_them():
     y, mag = P.mx4_product(P.mx4_values(a[0], a[1]), P.mx4_values(a[2], a[3]), torch.tensor([0, 20, 50]))
     P.rounded(got, y, 128 * 2.0 ** -23 * mag)
     a[4] = torch.tensor([0, 40, 20], dtype=torch.int32)      # a decreasing pair: an empty segment
-    ops.mx4_matmul(*[t.cuda() for t in a])
+    out = torch.full((50, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    got = ops.mx4_matmul(*[t.cuda() for t in a], out=out)
     assert ops.status() == M.MOE_ERR_DEVICE_BOUNDS
+    y, mag = P.mx4_product(P.mx4_values(a[0], a[1]), P.mx4_values(a[2], a[3]), torch.tensor([0, 40, 40]))
+    P.rounded(got[:40], y[:40], 128 * 2.0 ** -23 * mag[:40])
+    assert (got[40:] == 7.0).all()
+
+
+def test_matmul_keeps_segments_of_unsound_offsets_apart():
+    """Offsets that swing up and down: an expert starts at the largest offset so far, so no row has two experts."""
+    E = 200
+    a = list(matmul_inputs([0] * (E - 1) + [90], 128, 64, seed=11))
+    a[4] = torch.tensor([(0, 90, 30, 60)[e % 4] for e in range(E + 1)], dtype=torch.int32)
+    got = ops.mx4_matmul(*[t.cuda() for t in a])
+    assert ops.status() == M.MOE_ERR_DEVICE_BOUNDS
+    y, mag = P.mx4_product(P.mx4_values(a[0], a[1]), P.mx4_values(a[2], a[3]), torch.tensor([0] + [90] * E))
+    P.rounded(got, y, 64 * 2.0 ** -23 * mag)
 
 
 # ---- together ------------------------------------------------------------------------------------
@@ -528,6 +546,31 @@ def test_captured_in_a_graph_and_replayed_on_new_inputs():
         for i, (p, q) in enumerate(zip(held, again)):
             assert torch.equal(p[:kept], q[:kept]) if i in (0, 7) else torch.equal(p, q), i
     assert ops.status() == M.MOE_OK
+
+
+def test_captured_by_a_process_that_made_no_call_before():
+    """The kernels are loaded while the capture runs."""
+    code = """
+import sys
+sys.path[:0] = [%r, %r]
+import torch
+from bit_grouped_expert_router_b200 import ops
+x, idx = torch.randn(700, 64, device="cuda"), torch.zeros(700, 8, dtype=torch.int32, device="cuda")
+w, ws = torch.zeros(2, 16, 32, dtype=torch.uint8, device="cuda"), torch.zeros(2, 16, 2, dtype=torch.uint8, device="cuda")
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    d = ops.dispatch_rows(x, idx, 2)
+    c, s = ops.mx4_quantize(x, pos=d.pos)
+    y = ops.mx4_matmul(c, s, w, ws, d.offsets)
+    n = ops.block_norm(x, x, norm_post=True, w_post=x[0].clone())
+    b = ops.block_norm_backward(n.n, n.h, n.h, x, r_pre=n.r_pre, r_post=n.r_post, w_post=x[0].clone())
+g.replay()
+torch.cuda.synchronize()
+assert ops.status() == 0 and torch.equal(d.rows[5599], x[699]) and (y == 0).all()
+print("captured")
+""" % (os.path.dirname(os.path.dirname(os.path.abspath(__file__))), os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout + r.stderr
 
 
 def test_offsets_and_perm_are_those_of_moe_route():
