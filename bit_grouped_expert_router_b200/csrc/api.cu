@@ -22,6 +22,7 @@
 #include "../../include/moe.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "ops.h"
 
 using namespace moe;
 

@@ -154,11 +154,6 @@ int gemm_tile_rows(int T, int k, int E);
 // host-side error text for moe_last_error() (defined in api.cu)
 void set_last_error(const char* msg);
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn tensor_map_encode_fn();   // cuTensorMapEncodeTiled (defined in api.cu; NULL if unavailable)
-
 // decode sparse GEMV
 // tm: 1 (the single-token form) or kDecodeFusedMaxT (1..kDecodeFusedMaxT tokens per launch)
 bool decode_fused_geometry(int H, int I, int E, int k, int has_shared, int tm, DecodeGeom* out);

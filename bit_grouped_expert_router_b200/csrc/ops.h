@@ -8,6 +8,11 @@
 
 namespace moe {
 
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn tensor_map_encode_fn();   // cuTensorMapEncodeTiled (defined in api.cu; NULL if unavailable)
+
 // ---- rows.cu: pairs sorted by expert, rows moved there and back -----------------------------------
 constexpr int kSortThreads = 1024;       // pairs ranked at a time by one CTA of the general sort
 constexpr int kSortMaxChunks = 148;      // the tokens are split into at most this many chunks (one CTA per SM)
