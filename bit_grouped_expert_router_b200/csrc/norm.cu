@@ -472,7 +472,10 @@ template <typename F> cudaError_t with_width(int H, F f) {
     if (H <= 8192) return f(Geom<8, 4>());
     return f(Geom<16, 4>());
 }
-// Few rows (fewer than warps to fill the SMs): as many warps per row as its values allow.
+// Few rows, bound by the latency of one: as many warps per row as its values allow.  Few / many rows' choice, in us
+// (both norms, bf16): 512 x 2048 3.0 / 3.2 and 2048 x 2048 8.3 / 8.5, 128 x 1024 2.1 / 3.6 and 2048 x 1024 4.3 / 4.5,
+// 1024 x 512 2.5 / 2.8 and 2048 x 512 4.0 / 3.1, 256 x 4096 3.1 / 4.2 and 1024 x 4096 9.3 / 7.6.
+bool many_rows(int T, int H) { return T >= 2048 || (long long)T * H >= 1 << 21; }
 template <typename F> cudaError_t with_width_few(int H, F f) {
     if (H <= 256) return f(Geom<1, 1>());
     if (H <= 512) return f(Geom<2, 1>());
@@ -503,7 +506,7 @@ cudaError_t launch_block_norm(const NormArgs& a, int h_dtype, int y_dtype, cudaS
             return launch_pdl(block_norm_kernel<decltype(th), decltype(ty), W::G, W::V>,
                               dim3((a.T + C::kRows - 1) / C::kRows), dim3(C::kThreads), 0, st, a);
         };
-        return (long long)a.T * a.H >= kNormManyValues ? with_width(a.H, launch) : with_width_few(a.H, launch);
+        return many_rows(a.T, a.H) ? with_width(a.H, launch) : with_width_few(a.H, launch);
     });
 }
 

@@ -72,7 +72,6 @@ struct NormArgs {
     int T, H, norm_post;
     float scale, eps;
 };
-constexpr long long kNormManyValues = 1 << 20;   // from here on the rows alone fill the SMs
 cudaError_t launch_block_norm(const NormArgs& a, int h_dtype, int y_dtype, cudaStream_t st);
 
 constexpr int kNormBwdCtas = 148;   // most blocks of the backward pass (one per SM)
