@@ -224,24 +224,38 @@ struct Unit {
 // unit, in every warp, cost 0.3 us of the 2.3 us between units of two steps).
 template <int TN> struct UnitWalk {
     const int *ustart, *seg, *len;   // first unit of an expert, its first row, its rows
+    const Unit* first;               // the CTA's first unit, found while the list was made
     int E, MT, total, stride, u;
     int n = 0;
     Unit mine = {0, 0, 0, 0};
 
     __device__ bool more() const { return u < total; }
     __device__ Unit next() {
-        const int k = n & 31;
-        if (k == 0) {
+        const int k = (n - 1) & 31;
+        if (n > 0 && k == 0) {
             const uint32_t v = (uint32_t)u + lane_id() * (uint32_t)stride;
             if (v < (uint32_t)total) mine = find((int)v);
         }
-        ++n;
         u += stride;
+        if (n++ == 0) return *first;
         Unit r;
         r.e = __shfl_sync(0xffffffffu, mine.e, k);
         r.mt = __shfl_sync(0xffffffffu, mine.mt, k);
         r.row0 = __shfl_sync(0xffffffffu, mine.row0, k);
         r.rows = __shfl_sync(0xffffffffu, mine.rows, k);
+        return r;
+    }
+
+    // Unit w of expert e, which has `rows` rows from `row` on.
+    static __device__ Unit unit_of(int e, int w, int row, int rows, int MT) {
+        const int groups = (rows + 15) / 16, tiles = (rows + TN - 1) / TN, tile = w / MT;
+        const int each = groups / tiles, left = groups - each * tiles;   // the first `left` tiles have one group more
+        const int g0 = each * tile + min(tile, left), g1 = g0 + each + (tile < left ? 1 : 0);
+        Unit r;
+        r.e = e;
+        r.mt = w - tile * MT;
+        r.row0 = row + 16 * g0;
+        r.rows = min(rows, 16 * g1) - 16 * g0;
         return r;
     }
 
@@ -253,16 +267,7 @@ private:
             if (ustart[mid] <= v) lo = mid;
             else hi = mid;
         }
-        const int rows = len[lo], groups = (rows + 15) / 16, tiles = (rows + TN - 1) / TN;
-        const int w = v - ustart[lo], tile = w / MT;
-        const int each = groups / tiles, left = groups - each * tiles;   // the first `left` tiles have one group more
-        const int g0 = each * tile + min(tile, left), g1 = g0 + each + (tile < left ? 1 : 0);
-        Unit r;
-        r.e = lo;
-        r.mt = w - tile * MT;
-        r.row0 = seg[lo] + 16 * g0;
-        r.rows = min(rows, 16 * g1) - 16 * g0;
-        return r;
+        return unit_of(lo, v - ustart[lo], seg[lo], len[lo], MT);
     }
 };
 
@@ -359,6 +364,7 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[kRing], empty[kRing], sffull[kSfRing], sfempty[kSfRing], dfull[2], dempty[2], drain;
     __shared__ int ustart[257], seg[256], len[256], wsum[8];
+    __shared__ Unit first_unit;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_word;
     uint8_t* ring = smem_raw + (1024u - (smem_u32(smem_raw) & 1023u) & 1023u);
@@ -396,9 +402,13 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
     // offsets[0..e] to the largest of offsets[0..e+1], held to [0, R]: the offsets themselves if they are sound,
     // and disjoint segments whatever they are.
     const int MT = (a.N + kTM - 1) / kTM;
-    int mine = 0, inc = 0, low = 0, high = 0;
+    int mine = 0, inc = 0, low = 0, high = 0, o0 = 0, o1 = 0;
     if (tid < 256) {
-        low = tid < a.E ? min(max(a.offsets[tid], 0), a.R) : 0;
+        if (tid < a.E) {
+            o0 = a.offsets[tid];
+            o1 = a.offsets[tid + 1];
+        }
+        low = min(max(o0, 0), a.R);
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, low, off);
@@ -410,9 +420,8 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
     if (tid < 256) {
         for (int w = 0; w < warp; ++w) low = max(low, wsum[w]);
         if (tid < a.E) {
-            const int next = a.offsets[tid + 1];
-            high = max(low, min(next, a.R));
-            if (blockIdx.x == 0 && (low != a.offsets[tid] || high != next)) set_status(status, MOE_STATUS_BOUNDS);
+            high = max(low, min(o1, a.R));
+            if (blockIdx.x == 0 && (low != o0 || high != o1)) set_status(status, MOE_STATUS_BOUNDS);
             seg[tid] = low;
             len[tid] = high - low;
             mine = (high - low + TN - 1) / TN * MT;
@@ -433,10 +442,12 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
         for (int w = 0; w < warp; ++w) inc += wsum[w];
         if (tid < a.E) ustart[tid] = inc - mine;
         if (tid == a.E - 1) ustart[a.E] = inc;
+        if (inc - mine <= (int)blockIdx.x && (int)blockIdx.x < inc)
+            first_unit = UnitWalk<TN>::unit_of(tid, blockIdx.x - (inc - mine), low, high - low, MT);
     }
     __syncthreads();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);   // (uniform, to the compiler too)
-    UnitWalk<TN> walk{ustart, seg, len, a.E, MT, ustart[a.E], (int)gridDim.x, (int)blockIdx.x};
+    UnitWalk<TN> walk{ustart, seg, len, &first_unit, a.E, MT, ustart[a.E], (int)gridDim.x, (int)blockIdx.x};
     const int KS = (a.K + kStep - 1) / kStep;
 
     if (warp == 0) {
