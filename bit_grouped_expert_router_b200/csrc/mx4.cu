@@ -190,8 +190,8 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t* __r
 // 2 x 32 columns of scales, alternating by step.
 //
 // What bounds it: weights and results from and to HBM while the rows are few (results alone pass at the rate
-// of a fill, 3.9 TB/s), then the traffic from L2 (weights once per row tile, rows once per feature tile: 66 us
-// of 85 for 32768 x 1024 x 2048 with nothing but the loads, 9.9 TB/s), and, run after run, the power cap (1.65 GHz
+// of a fill, 3.9 TB/s), then the traffic from L2 (weights once per row tile, rows once per feature tile: 699 MB of it
+// in the 74 us of 32768 x 1024 x 2048 over 256 experts), and, run after run, the power cap (1.65 GHz and 87 us
 // there).  Pairs of CTAs on one tile of 256 features (cta_group::2), which read the rows half as often, gained
 // 3 to 5% from 131072 rows on and lost 1 to 30% below: their barriers and commits cross CTAs every step.
 constexpr int kTM = 128;             // features per unit
@@ -231,14 +231,16 @@ template <int TN> struct UnitWalk {
 
     __device__ bool more() const { return u < total; }
     __device__ Unit next() {
-        const int k = (n - 1) & 31;
-        if (n > 0 && k == 0) {
+        const int k = n == 0 ? 0 : (n - 1) & 31;
+        if (n == 0) {
+            mine = *first;
+        } else if (k == 0) {
             const uint32_t v = (uint32_t)u + lane_id() * (uint32_t)stride;
             if (v < (uint32_t)total) mine = find((int)v);
         }
+        ++n;
         u += stride;
-        if (n++ == 0) return *first;
-        Unit r;
+        Unit r;   // (exchanged, so that the compiler may keep it in uniform registers)
         r.e = __shfl_sync(0xffffffffu, mine.e, k);
         r.mt = __shfl_sync(0xffffffffu, mine.mt, k);
         r.row0 = __shfl_sync(0xffffffffu, mine.row0, k);

@@ -308,7 +308,7 @@ int moe_mx4_matmul(const uint8_t* codes, const uint8_t* scales, int32_t n_rows, 
     OPS_CHECK(K >= 32 && K % 32 == 0 && K <= kMaxMx4Width, "K must be a multiple of 32 in [32, %d] (got %d)", kMaxMx4Width, K);
     OPS_CHECK(E >= 1 && E <= 256, "E must be in [1, 256] (got %d)", E);
     OPS_CHECK(N >= 8 && N % 8 == 0 && (long long)E * N < (1ll << 31), "N must be a multiple of 8 with E * N < 2^31 (got %d)", N);
-    OPS_CHECK(((long long)n_rows / 64 + E) * ((N + 127) / 128) < (1ll << 31), "too many tiles: n_rows = %d, N = %d", n_rows, N);
+    OPS_CHECK(((long long)n_rows / 64 + E) * ((N + 127) / 128) < (1ll << 30), "too many tiles: n_rows = %d, N = %d", n_rows, N);
     if (n_rows == 0) return MOE_OK;
     OPS_CHECK(ok16(codes) && ok16(scales) && ok16(w_codes) && ok16(w_scales) && ok4(offsets) && ok16(y),
               "moe_mx4_matmul: a pointer is NULL or misaligned");
