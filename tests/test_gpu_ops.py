@@ -630,3 +630,18 @@ def test_tensors_that_do_not_fit_are_refused():
         ops.block_norm(x, eps=-1.0)
     assert e.value.code == M.MOE_ERR_INVALID_ARG and "eps" in str(e.value)
     assert ops.status() == M.MOE_OK
+
+
+def test_product_past_32_bit_offsets():
+    """Results beyond 2^31 elements: the last rows land where they belong."""
+    R, N, K = 270000, 8192, 32
+    codes = torch.full((R, K // 2), 0x22, dtype=torch.uint8, device="cuda")          # ones
+    scales = (126 + torch.arange(R, device="cuda") % 4).to(torch.uint8).view(R, 1)
+    w = torch.full((1, N, K // 2), 0x22, dtype=torch.uint8, device="cuda")
+    ws = (126 + torch.arange(N, device="cuda") % 3).to(torch.uint8).view(1, N, 1)
+    y = ops.mx4_matmul(codes, scales, w, ws, torch.tensor([0, R], dtype=torch.int32, device="cuda"))
+    assert y.numel() > 1 << 31
+    rows = torch.tensor([0, 1, R // 2, (1 << 31) // N, R - 2, R - 1], device="cuda")
+    want = 32.0 * torch.exp2((rows % 4 - 1).float()).view(-1, 1) * torch.exp2((torch.arange(N, device="cuda") % 3 - 1).float())
+    assert torch.equal(y[rows].float(), want)
+    assert ops.status() == M.MOE_OK
