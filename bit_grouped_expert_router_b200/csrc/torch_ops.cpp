@@ -117,7 +117,8 @@ ScalarType scalar_type(int dtype) {
 }
 
 int32_t small(int64_t n, const char* name) {
-    if (n > std::numeric_limits<int32_t>::max()) throw Refused(std::string(name) + ": too large");
+    if (n > std::numeric_limits<int32_t>::max() || n < std::numeric_limits<int32_t>::min())
+        throw Refused(std::string(name) + ": does not fit 32 bits");
     return (int32_t)n;
 }
 // Sizes of a matrix.
@@ -144,6 +145,15 @@ float real(PyObject* o, const char* name) {
         throw Refused(std::string(name) + ": a number is needed");
     }
     return (float)v;
+}
+
+bool truth(PyObject* o, const char* name) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) {
+        PyErr_Clear();
+        throw Refused(std::string(name) + ": a truth value is needed");
+    }
+    return v > 0;
 }
 
 Tensor empty(IntArrayRef shape, ScalarType st, int dev) {
@@ -188,7 +198,7 @@ PyObject* dispatch_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
         } else if (into) {
             throw Refused("rows needs x");
         }
-        Tensor offsets = empty({E + 1}, at::kInt, dev), perm = empty({pairs}, at::kInt, dev), pos = empty({T, k}, at::kInt, dev);
+        Tensor offsets = empty({(int64_t)E + 1}, at::kInt, dev), perm = empty({pairs}, at::kInt, dev), pos = empty({T, k}, at::kInt, dev);
         const size_t need = moe_dispatch_workspace(T, k, E);
         Tensor ws;
         if (need) ws = empty({(int64_t)need}, at::kByte, dev);
@@ -277,7 +287,7 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
                      *w_post = optional_tensor(a[3], "w_post"), *gate = optional_tensor(a[4], "gate"),
                      *h_into = optional_tensor(a[9], "h_out"), *n_into = optional_tensor(a[10], "n_out");
         const float scale = real(a[5], "scale"), eps = real(a[6], "eps");
-        const bool norm_post = PyObject_IsTrue(a[7]) > 0, pre = PyObject_IsTrue(a[11]) > 0;
+        const bool norm_post = truth(a[7], "norm_post"), pre = truth(a[11], "pre");
         const int given = integer(a[8], "n_dtype");
         const int dev = device_of(h, "h");
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
@@ -356,6 +366,7 @@ PyObject* mx4_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int dt = rows_dtype(x.scalar_type(), "x");
         void* xp = at_of(&x, "x", x.scalar_type(), {T, W}, dev);
         const int32_t k = pos ? matrix(*pos, "pos").second : 1;
+        if (k < 1) throw Refused("pos: at least one place per token is needed");   // (its address would be NULL)
         const auto* pp = at_of<int32_t>(pos, "pos", at::kInt, {T, k}, dev);
         const int32_t rows = c_into ? matrix(*c_into, "codes").first : small((int64_t)T * k, "pos");
         Tensor codes = c_into ? *c_into : empty({rows, K / 2}, at::kByte, dev);
@@ -405,7 +416,7 @@ PyObject* mx4_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const auto* sp = at_of<uint8_t>(&scales, "scales", at::kByte, {R, Kh / 16}, dev);
         const auto* wp = at_of<uint8_t>(&w_codes, "w_codes", at::kByte, {E, N, Kh}, dev);
         const auto* wq = at_of<uint8_t>(&w_scales, "w_scales", at::kByte, {E, N, Kh / 16}, dev);
-        const auto* fp = at_of<int32_t>(&offsets, "offsets", at::kInt, {E + 1}, dev);
+        const auto* fp = at_of<int32_t>(&offsets, "offsets", at::kInt, {(int64_t)E + 1}, dev);
         Tensor out = into ? *into : empty({R, N}, scalar_type(dt), dev);
         void* op = at_of(&out, "out", out.scalar_type(), {R, N}, dev);
         check(moe_mx4_matmul(cp, sp, R, K, wp, wq, E, N, fp, op, rows_dtype(out.scalar_type(), "out"), stream_of(dev)));

@@ -645,3 +645,24 @@ def test_product_past_32_bit_offsets():
     want = 32.0 * torch.exp2((rows % 4 - 1).float()).view(-1, 1) * torch.exp2((torch.arange(N, device="cuda") % 3 - 1).float())
     assert torch.equal(y[rows].float(), want)
     assert ops.status() == M.MOE_OK
+
+
+def test_integers_and_truths_that_do_not_fit_are_refused():
+    idx = torch.zeros((2, 1), dtype=torch.int32, device="cuda")
+    x = torch.ones((2, 64), device="cuda")
+    for E in (2 ** 32 + 4, -2 ** 32 + 4):   # 4 in the low 32 bits
+        with pytest.raises(ValueError, match="E"):
+            ops.dispatch_rows(None, idx, E)
+    for name in ("norm_post", "pre"):
+        with pytest.raises(ValueError, match=name):
+            ops.block_norm(x, y=x.clone(), **{name: torch.ones(2)})
+
+
+def test_quantize_to_no_places_is_refused():
+    """pos [T, 0] has no address: it must not pass for an absent pos, whose rows go to the rows of their own."""
+    x = torch.ones((3, 64), device="cuda")
+    codes = torch.full((3, 32), 0x99, dtype=torch.uint8, device="cuda")
+    scales = torch.full((3, 2), 0x99, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="pos"):
+        ops.mx4_quantize(x, pos=torch.zeros((3, 0), dtype=torch.int32, device="cuda"), codes=codes, scales=scales)
+    assert (codes == 0x99).all() and (scales == 0x99).all()
