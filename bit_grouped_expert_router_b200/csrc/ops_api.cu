@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cstdarg>
 #include <cstdio>
+#include <mutex>
 
 #include "../../include/moe.h"
 #include "common.cuh"
@@ -108,7 +109,10 @@ int moe_ops_status(void* stream) {
     (void)sms;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint32_t a = 0, b = 0, c = 0;
-    cudaError_t e = rows_take_status(&a, st);
+    cudaError_t e = cudaStreamSynchronize(st);
+    static std::mutex one;   // a call's taken word is read before another call's take replaces it
+    const std::lock_guard<std::mutex> lock(one);
+    if (e == cudaSuccess) e = rows_take_status(&a, st);
     if (e == cudaSuccess) e = norm_take_status(&b, st);
     if (e == cudaSuccess) e = mx4_take_status(&c, st);
     if (e != cudaSuccess) return launched("moe_ops_status", e);

@@ -666,3 +666,27 @@ def test_quantize_to_no_places_is_refused():
     with pytest.raises(ValueError, match="pos"):
         ops.mx4_quantize(x, pos=torch.zeros((3, 0), dtype=torch.int32, device="cuda"), codes=codes, scales=scales)
     assert (codes == 0x99).all() and (scales == 0x99).all()
+
+
+def test_an_error_is_told_once_to_one_of_two_callers():
+    """Two threads take the status at a time: one of them gets the error, whoever comes first."""
+    idx = torch.full((1, 1), 9, dtype=torch.int32, device="cuda")   # no expert of four
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    start = threading.Barrier(2, timeout=60)
+    got = [[], []]
+
+    def take(i):
+        for _ in range(100):
+            start.wait()
+            if i == 0:
+                ops.dispatch_rows(None, idx, 4)
+                torch.cuda.current_stream().synchronize()
+            start.wait()
+            got[i].append(ops.status(streams[i]))
+
+    threads = [threading.Thread(target=take, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert all(sorted(pair) == sorted((M.MOE_OK, M.MOE_ERR_DEVICE_BOUNDS)) for pair in zip(*got))
