@@ -12,8 +12,7 @@ namespace {
 
 // ---- quantisation ---------------------------------------------------------------------------------
 // Two neighbouring threads share a block of 32 values, sixteen each: their largest magnitude by one
-// exchange, eight bytes of codes per thread; two such items per thread, so four 16-byte loads (eight
-// with SwiGLU) are in flight.  Codes and scales of consecutive blocks lie next to each other, so rows
+// exchange, eight bytes of codes per thread.  Codes and scales of consecutive blocks lie next to each other, so rows
 // matter only where they are halved (SwiGLU) or sent elsewhere (pos: a token is read and quantised once
 // and written to all of its places).  Bound by those bytes: 131072 x 512 bf16 in 25.8 us.
 
@@ -53,18 +52,30 @@ template <typename T> __device__ __forceinline__ uint32_t top_bits(const Vec<T, 
     return __float_as_uint(lo);
 }
 
-// 1 / x to one unit in the last place (32768 x 512 outputs of SwiGLU: 19.3 us; with the exact quotient 21.8 us).
+// 1 / x to one unit in the last place, x >= 1; 0 for x above 2^126, where the quotient is no normal number: silu's
+// tail is 0 from -87.3 on instead of -88.7, where expf ends (32768 x 512 outputs of SwiGLU: 15.7 us; with the
+// instruction that keeps subnormal quotients, and the largest magnitude taken in integers, 19.0 us).
 __device__ __forceinline__ float reciprocal(float x) {
     float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// max(a, |b|), NaN if either is.
+__device__ __forceinline__ float max_magnitude(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
     return r;
 }
 
-constexpr int kQuantItems = 2;   // per thread
+// Items per thread: two, so that enough loads are in flight, but one where the places add loads and most bytes are
+// written (4096 and 16384 tokens of 2048 to 8 rows each: 10.7 and 35.9 us with one item, 11.8 and 39.7 with two;
+// 131072 x 512 in order: 26.0 and 25.7 us).
+__host__ __device__ constexpr int quant_items(bool pos) { return pos ? 1 : 2; }
 template <typename T, bool SWIGLU, bool POS>
 __global__ void __launch_bounds__(256) mx4_quantize_kernel(Mx4QuantArgs a, uint32_t items) {
     griddep_wait();
     griddep_launch_dependents();
+    constexpr int kQuantItems = quant_items(POS);
     const uint32_t n = (uint32_t)a.K / 16;   // items of sixteen values per row: even, like all counts here
     const uint32_t i0 = blockIdx.x * (256u * kQuantItems) + threadIdx.x;
     Vec<T, 8> x[kQuantItems][2], up[SWIGLU ? kQuantItems : 1][2];
@@ -93,14 +104,15 @@ __global__ void __launch_bounds__(256) mx4_quantize_kernel(Mx4QuantArgs a, uint3
             if constexpr (SWIGLU) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float g[8], p[8];
+                    float g[8], p[8], most = 0.f;
                     x[u][h].get(g);
                     up[u][h].get(p);
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
                         v[h][q] = g[q] * reciprocal(1.f + expf(-g[q])) * p[q];
-                        top = max(top, __float_as_uint(v[h][q]) & 0x7FFFFFFFu);
+                        most = max_magnitude(most, v[h][q]);
                     }
+                    top = max(top, __float_as_uint(most));
                 }
             } else {
                 top = top_bits(x[u]);
@@ -656,7 +668,7 @@ __global__ void __launch_bounds__(kThreadsMm, 1) mx4_matmul_kernel(Mx4MatmulArgs
 }  // namespace
 
 cudaError_t launch_mx4_quantize(const Mx4QuantArgs& a, int dtype, cudaStream_t st) {
-    const uint32_t items = (uint32_t)((size_t)a.T * (a.K / 16)), per = 256 * kQuantItems;
+    const uint32_t items = (uint32_t)((size_t)a.T * (a.K / 16)), per = 256 * quant_items(a.pos);
     const dim3 grid((items + per - 1) / per);
     return with_dtype(dtype, [&](auto t) {
         using T = decltype(t);

@@ -690,3 +690,21 @@ def test_an_error_is_told_once_to_one_of_two_callers():
     for t in threads:
         t.join()
     assert all(sorted(pair) == sorted((M.MOE_OK, M.MOE_ERR_DEVICE_BOUNDS)) for pair in zip(*got))
+
+
+def test_swiglu_at_the_ends_of_its_range():
+    """Blocks of one value each: the gate's tails, and infinities and NaN in either half."""
+    inf, nan = math.inf, math.nan
+    pairs = [(100.0, 3.0), (-100.0, 3.0), (-88.0, 1.0), (-80.0, 2.0), (1e30, 1e5), (1e30, 1e10), (-inf, 1.0), (inf, 2.0),
+             (1.0, inf), (1.0, -inf), (nan, 1.0), (1.0, nan), (0.0, inf), (-0.0, 5.0), (0.0, 0.0)]
+    x = torch.tensor([[0.0] * 31 + [g] + [0.0] * 31 + [u] for g, u in pairs])
+    codes, scales = ops.mx4_quantize(x.cuda(), act="swiglu")
+    got = ops.mx4_dequantize(codes, scales, torch.float32).cpu()[:, 31].tolist()
+    for (g, u), y in zip(pairs, got):
+        v = g / (1 + math.exp(-g)) * u if -700 < g < 1e300 else (nan if g == -inf else g * u)
+        if not abs(v) <= torch.finfo(torch.float32).max:
+            assert math.isnan(y), (g, u, y)
+        elif abs(v) < 2.0 ** -119:   # the tail: 0, or the value where it is still one of fp32
+            assert abs(y) <= 1.5 * abs(v), (g, u, y)
+        else:                        # the largest of its block lies in [4, 8) of the scale and goes to 4 or 6
+            assert abs(y - v) <= abs(v) / 4, (g, u, y)
