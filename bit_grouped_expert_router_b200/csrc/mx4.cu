@@ -14,7 +14,7 @@ namespace {
 // Two neighbouring threads share a block of 32 values, sixteen each: their largest magnitude by one
 // exchange, eight bytes of codes per thread.  Codes and scales of consecutive blocks lie next to each other, so rows
 // matter only where they are halved (SwiGLU) or sent elsewhere (pos: a token is read and quantised once
-// and written to all of its places).  Bound by those bytes: 131072 x 512 bf16 in 25.8 us.
+// and written to all of its places).  Bound by those bytes: 131072 x 512 bf16 in 25.7 us.
 
 // Two values as E2M1 codes (round to nearest, ties to even, magnitudes above 6 to 6), the first in the
 // low four bits; eight of them as a word.
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t* __r
 //
 // What bounds it: weights and results from and to HBM while the rows are few (results alone pass at the rate
 // of a fill, 3.9 TB/s), then the traffic from L2 (weights once per row tile, rows once per feature tile: 699 MB of it
-// in the 74 us of 32768 x 1024 x 2048 over 256 experts), and, run after run, the power cap (1.65 GHz and 87 us
+// in the 73 us of 32768 x 1024 x 2048 over 256 experts), and, run after run, the power cap (1.65 GHz and 87 us
 // there).  Pairs of CTAs on one tile of 256 features (cta_group::2), which read the rows half as often, gained
 // 3 to 5% from 131072 rows on and lost 1 to 30% below: their barriers and commits cross CTAs every step.
 constexpr int kTM = 128;             // features per unit
@@ -703,8 +703,9 @@ static cudaError_t launch_matmul(const Mx4MatmulArgs& a, const CUtensorMap& tm_w
 
 cudaError_t launch_mx4_matmul(const Mx4MatmulArgs& a, const CUtensorMap& tm_w, const CUtensorMap& tm_x, int dtype,
                               int num_sms, cudaStream_t st) {
-    // Row tiles of 64 up to 32 rows per expert on average: 256 experts of 1024 x 2048 with 1 to 32 rows each 45 to 56 us
-    // with them, 49 to 60 us with 224; with 64 rows each 85 and 71 us.
+    // Row tiles of 64 up to 32 rows per expert on average.  256 experts of 1024 x 2048, tiles of 64 / of 224, in us:
+    // 1 row each 46.7 / 49.6, 8 rows 48.6 / 51.1, 32 rows 51.7 / 53.0 (in uneven segments 58.0 / 55.9), 64 rows
+    // 56.8 / 56.6 (71.8 / 61.3), 96 rows 84.5 / 61.1.
     const bool few = a.R <= 32ll * a.E;
     if (dtype == MOE_DTYPE_BF16)
         return few ? launch_matmul<__nv_bfloat16, 64>(a, tm_w, tm_x, num_sms, st)
