@@ -708,3 +708,16 @@ def test_swiglu_at_the_ends_of_its_range():
             assert abs(y) <= 1.5 * abs(v), (g, u, y)
         else:                        # the largest of its block lies in [4, 8) of the scale and goes to 4 or 6
             assert abs(y - v) <= abs(v) / 4, (g, u, y)
+
+
+@pytest.mark.parametrize("T,k,K", [(1, 1, 32), (37, 3, 544), (300, 9, 96)])
+def test_swiglu_quantize_into_sorted_rows(T, k, K):
+    """The activation sent to places gives what the activation in order gives there."""
+    g = gen(T, k, K, 11)
+    x = torch.randn((T, 2 * K), generator=g).bfloat16().cuda()
+    d = ops.dispatch_rows(None, draw_idx(g, T, k, 7, 0.2).cuda(), 7)
+    codes, scales = ops.mx4_quantize(x, pos=d.pos, act="swiglu")
+    c, s = ops.mx4_quantize(x, act="swiglu")
+    kept = int(d.offsets[7])
+    of = d.perm[:kept].long() // k
+    assert torch.equal(codes[:kept], c[of]) and torch.equal(scales[:kept], s[of])
