@@ -4,6 +4,8 @@
 // Blocks of 32 values along a row share a scale 2^(s - 127); each value is a 4-bit E2M1 number times
 // it.  The product's operands go to the tensor core as they are stored: kind::mxf4 multiplies the
 // 4-bit values and applies both scales per 32 columns, accumulating in fp32.
+#include <type_traits>
+
 #include "ops_common.cuh"
 
 namespace moe {
@@ -52,13 +54,45 @@ template <typename T> __device__ __forceinline__ uint32_t top_bits(const Vec<T, 
     return __float_as_uint(lo);
 }
 
-// 1 / x to one unit in the last place, x >= 1; 0 for x above 2^126, where the quotient is no normal number: silu's
-// tail is 0 from -87.3 on instead of -88.7, where expf ends (32768 x 512 outputs of SwiGLU: 15.7 us; with the
-// instruction that keeps subnormal quotients, and the largest magnitude taken in integers, 19.0 us).
+// 1 / x to one unit in the last place, for x in [1, 2^126]: neither it nor the quotient is subnormal there, so the
+// instruction that flushes those gives what the one that keeps them gives, in fewer steps (32768 x 512 outputs of
+// SwiGLU: 15.5 us; with that one, and the largest magnitude taken in integers, 19.0 us).
 __device__ __forceinline__ float reciprocal(float x) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+// silu(g) u = g u / (1 + exp(-g)).  Below kSiluTail (exp(64) < 2^93 lies inside the reciprocal's range) 1 + exp(-g) is
+// exp(-g) to fp32's last bit, and the quotient alone would end at -87 though a large u can bring the product back into
+// range: there it is g exp(g / 2) u exp(g / 2), whose factors are ordinary numbers down to -174.
+constexpr float kSiluTail = -64.f;
+template <bool TAIL> __device__ __forceinline__ float silu_times(float g, float u) {
+    if (TAIL && g < kSiluTail) {
+        const float h = expf(0.5f * g);
+        return g * h * u * h;
+    }
+    return g * reciprocal(1.f + expf(-g)) * u;
+}
+// Whether a value is below kSiluTail (a negative NaN may pass for one), by its bits: those of negative numbers
+// order by magnitude, above all positive ones.
+__device__ __forceinline__ bool below_tail(const Vec<float, 8> (&x)[2]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint4 q = x[i >> 1].w[i & 1];
+        m = max(max(m, max(q.x, q.y)), max(q.z, q.w));
+    }
+    return m > 0xC2800000u;
+}
+template <typename T> __device__ __forceinline__ bool below_tail(const Vec<T, 8> (&x)[2]) {
+    constexpr uint32_t kTail = std::is_same_v<T, __half> ? 0xD400u : 0xC280u;
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint4 q = x[i].w[0];
+        m = __vmaxu2(__vmaxu2(m, __vmaxu2(q.x, q.y)), __vmaxu2(q.z, q.w));
+    }
+    return max(m >> 16, m & 0xFFFFu) > kTail;
 }
 // max(a, |b|), NaN if either is.
 __device__ __forceinline__ float max_magnitude(float a, float b) {
@@ -71,29 +105,15 @@ __device__ __forceinline__ float max_magnitude(float a, float b) {
 // written (4096 and 16384 tokens of 2048 to 8 rows each: 10.7 and 35.9 us with one item, 11.8 and 39.7 with two;
 // 131072 x 512 in order: 26.0 and 25.7 us).
 __host__ __device__ constexpr int quant_items(bool pos) { return pos ? 1 : 2; }
-template <typename T, bool SWIGLU, bool POS>
-__global__ void __launch_bounds__(256) mx4_quantize_kernel(Mx4QuantArgs a, uint32_t items) {
-    griddep_wait();
-    griddep_launch_dependents();
+// The loaded items quantised and stored.
+template <typename T, bool SWIGLU, bool POS, bool TAIL>
+__device__ __forceinline__ void quantize_items(const Mx4QuantArgs& a, uint32_t items, uint32_t i0,
+                                               const Vec<T, 8> (&x)[quant_items(POS)][2],
+                                               const Vec<T, 8> (&up)[SWIGLU ? quant_items(POS) : 1][2],
+                                               const uint32_t (&tok)[quant_items(POS)],
+                                               const uint32_t (&col)[quant_items(POS)]) {
     constexpr int kQuantItems = quant_items(POS);
-    const uint32_t n = (uint32_t)a.K / 16;   // items of sixteen values per row: even, like all counts here
-    const uint32_t i0 = blockIdx.x * (256u * kQuantItems) + threadIdx.x;
-    Vec<T, 8> x[kQuantItems][2], up[SWIGLU ? kQuantItems : 1][2];
-    uint32_t tok[kQuantItems], col[kQuantItems];
-#pragma unroll
-    for (int u = 0; u < kQuantItems; ++u) {
-        const uint32_t i = i0 + u * 256u;
-        if (i >= items) continue;
-        tok[u] = SWIGLU || POS ? i / n : 0;
-        col[u] = SWIGLU || POS ? i - tok[u] * n : 0;
-        const T* at = static_cast<const T*>(a.x) +
-                      (SWIGLU ? (size_t)tok[u] * 2 * a.K + (size_t)col[u] * 16 : (size_t)i * 16);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            x[u][h].load(at + 8 * h);
-            if constexpr (SWIGLU) up[u][h].load(at + a.K + 8 * h);
-        }
-    }
+    const uint32_t n = (uint32_t)a.K / 16;
 #pragma unroll
     for (int u = 0; u < kQuantItems; ++u) {   // every thread takes part in the exchanges
         const uint32_t i = i0 + u * 256u;
@@ -109,7 +129,7 @@ __global__ void __launch_bounds__(256) mx4_quantize_kernel(Mx4QuantArgs a, uint3
                     up[u][h].get(p);
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
-                        v[h][q] = g[q] * reciprocal(1.f + expf(-g[q])) * p[q];
+                        v[h][q] = silu_times<TAIL>(g[q], p[q]);
                         most = max_magnitude(most, v[h][q]);
                     }
                     top = max(top, __float_as_uint(most));
@@ -159,6 +179,39 @@ __global__ void __launch_bounds__(256) mx4_quantize_kernel(Mx4QuantArgs a, uint3
             }
         }
     }
+}
+
+template <typename T, bool SWIGLU, bool POS>
+__global__ void __launch_bounds__(256) mx4_quantize_kernel(Mx4QuantArgs a, uint32_t items) {
+    griddep_wait();
+    griddep_launch_dependents();
+    constexpr int kQuantItems = quant_items(POS);
+    const uint32_t n = (uint32_t)a.K / 16;   // items of sixteen values per row: even, like all counts here
+    const uint32_t i0 = blockIdx.x * (256u * kQuantItems) + threadIdx.x;
+    Vec<T, 8> x[kQuantItems][2], up[SWIGLU ? kQuantItems : 1][2];
+    uint32_t tok[kQuantItems], col[kQuantItems];
+#pragma unroll
+    for (int u = 0; u < kQuantItems; ++u) {
+        const uint32_t i = i0 + u * 256u;
+        if (i >= items) continue;
+        tok[u] = SWIGLU || POS ? i / n : 0;
+        col[u] = SWIGLU || POS ? i - tok[u] * n : 0;
+        const T* at = static_cast<const T*>(a.x) +
+                      (SWIGLU ? (size_t)tok[u] * 2 * a.K + (size_t)col[u] * 16 : (size_t)i * 16);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            x[u][h].load(at + 8 * h);
+            if constexpr (SWIGLU) up[u][h].load(at + a.K + 8 * h);
+        }
+    }
+    if constexpr (SWIGLU) {   // gates in silu's tail, rare, have a copy of the rest to themselves: a branch around each
+                              // activation, or the sum of exponentials that needs none, cost 1.7 to 2.4 of 15.5 us
+        bool tail = false;
+#pragma unroll
+        for (int u = 0; u < kQuantItems; ++u) tail |= i0 + u * 256u < items && below_tail(x[u]);
+        if (__any_sync(0xffffffffu, tail)) return quantize_items<T, SWIGLU, POS, true>(a, items, i0, x, up, tok, col);
+    }
+    quantize_items<T, SWIGLU, POS, false>(a, items, i0, x, up, tok, col);
 }
 
 // ---- values ---------------------------------------------------------------------------------------

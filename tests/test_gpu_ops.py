@@ -721,3 +721,26 @@ def test_swiglu_quantize_into_sorted_rows(T, k, K):
     kept = int(d.offsets[7])
     of = d.perm[:kept].long() // k
     assert torch.equal(codes[:kept], c[of]) and torch.equal(scales[:kept], s[of])
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_swiglu_keeps_the_tail_of_a_gate_whose_product_is_ordinary(dtype):
+    """silu(gate) far below one, times an up that brings it back: the value must not be lost on the way.  Each row's
+    second block is empty but for one value, the largest of its block: it lies in [4, 8) of the scale and goes to 4
+    or 6, so the result is within a quarter of it (and the few roundings on its way)."""
+    top = torch.finfo(dtype).max
+    pairs = [(g, u) for g in (-63.5, -64.0, -64.5, -80.0, -87.0, -87.5, -88.0, -88.5, -89.0, -92.0, -96.0, -100.0, -103.0)
+             for u in (1.0, 1e30, 1e36, -3e38) if abs(u) < top]
+    x = torch.zeros((len(pairs), 128))
+    for i, (g, u) in enumerate(pairs):
+        x[i, 63], x[i, 127] = g, u
+    x = x.to(dtype)
+    codes, scales = ops.mx4_quantize(x.cuda(), act="swiglu")
+    got = ops.mx4_dequantize(codes, scales, torch.float32).cpu().double()
+    assert (got[:, :63] == 0).all()
+    g, u = x[:, 63].double(), x[:, 127].double()
+    v = g * torch.exp(g) / (1 + torch.exp(g)) * u
+    held = v.abs() >= 2.0 ** -119          # below it the value ends under the smallest scale
+    assert int(held.sum()) >= (len(pairs) // 2 if dtype != torch.float16 else 4)
+    assert ((got[:, 63] - v).abs() <= v.abs() * (0.25 + 1e-6))[held].all()
+    assert (got[:, 63].abs() <= 1.5 * v.abs() + 2.0 ** -128)[~held].all()
