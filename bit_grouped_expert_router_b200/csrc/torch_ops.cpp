@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <initializer_list>
 #include <limits>
 #include <sstream>
 #include <stdexcept>
@@ -161,6 +162,13 @@ Tensor empty(IntArrayRef shape, ScalarType st, int dev) {
 }
 void* stream_of(int dev) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream(); }
 
+// Moves on the version of the tensors that the caller gave to be written: automatic differentiation finds out that
+// way that values it saved are gone.  (A tensor made in inference mode has no version.)
+void written(std::initializer_list<const Tensor*> given) {
+    for (const Tensor* t : given)
+        if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 PyObject* wrap(const Tensor& t) {
     if (!t.defined()) Py_RETURN_NONE;
     return THPVariable_Wrap(t);
@@ -204,6 +212,7 @@ PyObject* dispatch_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (need) ws = empty({(int64_t)need}, at::kByte, dev);
         check(moe_dispatch_rows(xp, dt, T, H, ip, k, E, rp, offsets.data_ptr<int32_t>(), perm.data_ptr<int32_t>(),
                                 pos.data_ptr<int32_t>(), need ? ws.data_ptr() : nullptr, need, stream_of(dev)));
+        written({into});
         return pack(rows, offsets, perm, pos);
     });
 }
@@ -225,6 +234,7 @@ PyObject* dispatch_rows_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         Tensor out = into ? *into : empty({T, H}, st, dev);
         void* op = at_of(&out, "out", st, {T, H}, dev);
         check(moe_dispatch_rows_backward(dp, dt, R, pp, T, k, H, op, stream_of(dev)));
+        written({into});
         return wrap(out);
     });
 }
@@ -248,6 +258,7 @@ PyObject* combine_weighted(PyObject*, PyObject* const* a, Py_ssize_t n) {
         Tensor out = into ? *into : empty({T, H}, st, dev);
         void* op = at_of(&out, "out", st, {T, H}, dev);
         check(moe_combine_weighted(rp, dt, R, pp, gp, T, k, H, bp, op, stream_of(dev)));
+        written({into});
         return wrap(out);
     });
 }
@@ -272,6 +283,7 @@ PyObject* combine_weighted_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
         Tensor drows = into ? *into : empty({R, H}, st, dev), dgates = empty({T, k}, at::kFloat, dev);
         void* dp = at_of(&drows, "drows", st, {R, H}, dev);
         check(moe_combine_weighted_backward(op, dt, rp, R, pp, gp, T, k, H, dp, dgates.data_ptr<float>(), stream_of(dev)));
+        written({into});
         return pack(drows, dgates);
     });
 }
@@ -310,6 +322,7 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         check(moe_block_norm(hp, hd, yp, yd, T, H, wq, norm_post, gp, scale, wp, eps, op, np,
                              norm_post ? r_post.data_ptr<float>() : nullptr, pre ? r_pre.data_ptr<float>() : nullptr,
                              stream_of(dev)));
+        written({h_into, n_into});
         return pack(h_out, n_out, r_post, r_pre);
     });
 }
@@ -374,6 +387,7 @@ PyObject* mx4_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
         auto* cp = at_of<uint8_t>(&codes, "codes", at::kByte, {rows, K / 2}, dev);
         auto* sp = at_of<uint8_t>(&scales, "scales", at::kByte, {rows, K / 32}, dev);
         check(moe_mx4_quantize(xp, dt, T, K, act, pp, k, rows, cp, sp, stream_of(dev)));
+        written({c_into, s_into});
         return pack(codes, scales);
     });
 }
@@ -420,6 +434,7 @@ PyObject* mx4_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
         Tensor out = into ? *into : empty({R, N}, scalar_type(dt), dev);
         void* op = at_of(&out, "out", out.scalar_type(), {R, N}, dev);
         check(moe_mx4_matmul(cp, sp, R, K, wp, wq, E, N, fp, op, rows_dtype(out.scalar_type(), "out"), stream_of(dev)));
+        written({into});
         return wrap(out);
     });
 }

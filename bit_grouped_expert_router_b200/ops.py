@@ -9,7 +9,8 @@ one device, run there on ``stream`` (default: that device's current stream) with
 what they return, and their scratch, on that stream unless an output tensor is given.  A wrong tensor raises
 ValueError, a refusal by the library MoeError; what the kernels find on the device is kept for ``status``.
 Tensors passed with ``stream`` must be ready there and stay alive until the stream has passed the call.  No graph of
-automatic differentiation is recorded: the gradients are functions of their own.
+automatic differentiation is recorded, not even for tensors that require gradients: the gradients are functions of their
+own.  A tensor given to be written counts as modified in place, so a graph that had saved its values refuses to use them.
 There is no fallback: if the module has not been built, the first call fails loudly.
 """
 from __future__ import annotations

@@ -744,3 +744,39 @@ def test_swiglu_keeps_the_tail_of_a_gate_whose_product_is_ordinary(dtype):
     assert int(held.sum()) >= (len(pairs) // 2 if dtype != torch.float16 else 4)
     assert ((got[:, 63] - v).abs() <= v.abs() * (0.25 + 1e-6))[held].all()
     assert (got[:, 63].abs() <= 1.5 * v.abs() + 2.0 ** -128)[~held].all()
+
+
+def test_a_tensor_given_to_be_written_is_modified_for_autograd():
+    """A graph that saved the buffer's values must refuse them, as after any in-place operation."""
+    T, k, H = 3, 2, 64
+    rand = lambda *s: torch.rand(s, device="cuda")  # noqa: E731
+    idx = torch.zeros((T, k), dtype=torch.int32, device="cuda")
+    pos = torch.arange(T * k, dtype=torch.int32, device="cuda").view(T, k)
+    codes, scales = ops.mx4_quantize(rand(T, H))
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    w, off = ops.mx4_quantize(rand(16, H)), torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    calls = {"rows": (rand(T * k, H), lambda b: ops.dispatch_rows(rand(T, H), idx, 1, rows=b)),
+             "dx": (rand(T, H), lambda b: ops.dispatch_rows_backward(rand(T * k, H), pos, out=b)),
+             "out": (rand(T, H), lambda b: ops.combine_weighted(rand(T * k, H), pos, rand(T, k), out=b)),
+             "drows": (rand(T * k, H), lambda b: ops.combine_weighted_backward(rand(T, H), rand(T * k, H), pos, rand(T, k), drows=b)),
+             "h_out": (rand(T, H), lambda b: ops.block_norm(rand(T, H), rand(T, H), h_out=b)),
+             "n_out": (rand(T, H), lambda b: ops.block_norm(rand(T, H), n_out=b)),
+             "y": (rand(T, 16), lambda b: ops.mx4_matmul(codes, scales, w[0].view(1, 16, -1), w[1].view(1, 16, -1), off, out=b)),
+             "codes": (u8(T, H // 2), lambda b: ops.mx4_quantize(rand(T, H), codes=b)),
+             "scales": (u8(T, H // 32), lambda b: ops.mx4_quantize(rand(T, H), scales=b))}
+    for name, (buffer, call) in calls.items():
+        if buffer.is_floating_point():
+            leaf = torch.ones_like(buffer, requires_grad=True)
+            loss = (leaf * buffer).sum()
+            call(buffer)
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                loss.backward()
+        else:
+            before = buffer._version
+            call(buffer)
+            assert buffer._version == before + 1, name
+    with torch.inference_mode():
+        made = torch.zeros((T, H), device="cuda")
+    ops.combine_weighted(rand(T * k, H), pos, torch.ones((T, k), device="cuda"), out=made)   # has no version
+    assert float(made.min()) > 0
+    assert ops.status() == M.MOE_OK
