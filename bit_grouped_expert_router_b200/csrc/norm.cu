@@ -510,6 +510,8 @@ cudaError_t launch_block_norm(const NormArgs& a, int h_dtype, int y_dtype, cudaS
     });
 }
 
+constexpr int kBwdSmem = 220 * 1024;   // dynamic shared memory of the backward pass; the static arrays have 7 KB beside it
+
 int norm_bwd_ctas(int T) { return T < kNormBwdCtas ? T : kNormBwdCtas; }
 
 cudaError_t launch_block_norm_bwd(const NormBwdArgs& a, int h_dtype, int y_dtype, cudaStream_t st) {
@@ -519,10 +521,11 @@ cudaError_t launch_block_norm_bwd(const NormBwdArgs& a, int h_dtype, int y_dtype
             using W = decltype(w);
             const int nh = a.H * (int)sizeof(th), ny = a.H * (int)sizeof(ty);
             BwdRing ring{0, nh, nh + ny, 2 * nh + ny, 2 * (nh + ny), 0};
-            const int room = 220 * 1024 - 8 * a.H;   // shared memory for the rings
+            const int room = kBwdSmem - 8 * a.H;   // for the rings, beside the weights
             int groups = BwdCfg<W::G>::kMaxGroups;
             auto kernel = block_norm_bwd_kernel<decltype(th), decltype(ty), W::G, W::V, false>;
-            size_t smem = W::G == 32 ? sizeof(float) * 2 * W::V * 8 * BwdCfg<W::G>::kMaxThreads : sizeof(float) * a.H;
+            constexpr int kSums = W::G == 32 ? (int)sizeof(float) * 2 * W::V * 8 * BwdCfg<W::G>::kMaxThreads : 0;
+            size_t smem = W::G == 32 ? kSums : sizeof(float) * a.H;
             if constexpr (W::G < 32) {
                 if (room / ring.stage_bytes >= 2) {
                     // two stages for as many groups as fit, then more stages
@@ -534,10 +537,11 @@ cudaError_t launch_block_norm_bwd(const NormBwdArgs& a, int h_dtype, int y_dtype
                     kernel = block_norm_bwd_kernel<decltype(th), decltype(ty), W::G, W::V, true>;
                 }
             }
-            if (smem > 36 * 1024) {   // with the static arrays, above 48 KB
-                const cudaError_t er = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-                if (er != cudaSuccess) return er;
-            }
+            // The most that any width of this kernel takes, not this call's size: the attribute belongs to the kernel, and
+            // another thread's call of another width may set it between this and the launch.
+            const cudaError_t er = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                        W::G == 32 ? kSums : kBwdSmem);
+            if (er != cudaSuccess) return er;
             return launch_pdl(kernel, dim3(ctas), dim3(groups * W::G * 32), smem, st, a, ring);
         });
     });

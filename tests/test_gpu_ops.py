@@ -780,3 +780,37 @@ def test_a_tensor_given_to_be_written_is_modified_for_autograd():
     ops.combine_weighted(rand(T * k, H), pos, torch.ones((T, k), device="cuda"), out=made)   # has no version
     assert float(made.min()) > 0
     assert ops.status() == M.MOE_OK
+
+
+def test_norm_gradients_of_two_widths_from_two_threads():
+    """The C entry points hold no lock: two threads may call one kernel, at widths that take different amounts of shared
+    memory, at the same time."""
+    L, calls = M.lib(), 20000
+    start, got, errors = threading.Barrier(2, timeout=60), [0, 0], []
+
+    def run(i, H):
+        try:
+            g = torch.Generator().manual_seed(H)
+            dn, h = (torch.randn((1, H), generator=g).bfloat16().cuda() for _ in range(2))
+            r, w, dw, dh = torch.ones(1, device="cuda"), torch.ones(H, device="cuda"), torch.empty(H, device="cuda"), torch.empty_like(h)
+            ws = torch.empty(L.moe_block_norm_backward_workspace(1, H), dtype=torch.uint8, device="cuda")
+            want = ops.block_norm_backward(dn, None, h, r_pre=r, w_pre=w)
+            s = torch.cuda.Stream()
+            torch.cuda.synchronize()
+            start.wait()
+            for _ in range(calls):
+                M.check(L.moe_block_norm_backward(dn.data_ptr(), None, h.data_ptr(), M.MOE_DTYPE_BF16, None, M.MOE_DTYPE_BF16, 1, H,
+                                                  r.data_ptr(), None, w.data_ptr(), None, 0, None, 1.0, dh.data_ptr(), None,
+                                                  dw.data_ptr(), None, None, ws.data_ptr(), ws.numel(), s.cuda_stream))
+                got[i] += 1
+            s.synchronize()
+            assert torch.equal(dh, want.dh) and torch.equal(dw, want.dw_pre)
+        except BaseException as e:
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i, H)) for i, H in enumerate((1032, 2048))]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    if errors:
+        raise errors[0]
+    assert got == [calls, calls] and ops.status() == M.MOE_OK
