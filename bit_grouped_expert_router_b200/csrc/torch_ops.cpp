@@ -58,6 +58,19 @@ template <typename F> PyObject* guarded(F f) {
     return nullptr;
 }
 
+// The interpreter's lock given up from here to end(), as in torch's own operators: allocations and launches may wait for
+// the device (a full launch queue, memory to be freed), and what the device waits for may be up to another thread.
+class Unlocked {
+    PyThreadState* held_ = PyEval_SaveThread();
+
+public:
+    void end() {
+        if (held_) PyEval_RestoreThread(held_);
+        held_ = nullptr;
+    }
+    ~Unlocked() { end(); }
+};
+
 void expect_args(Py_ssize_t have, Py_ssize_t want, const char* name) {
     if (have != want) throw Refused(std::string(name) + ": " + std::to_string(want) + " arguments are needed");
 }
@@ -187,10 +200,11 @@ PyObject* dispatch_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
         expect_args(n, 4, "dispatch_rows");
         const Tensor& idx = tensor(a[1], "idx");
         const Tensor *x = optional_tensor(a[0], "x"), *into = optional_tensor(a[3], "rows");
+        const int32_t E = integer(a[2], "E");
+        Unlocked unlocked;
         const int dev = device_of(idx, "idx");
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
         const auto [T, k] = matrix(idx, "idx");
-        const int32_t E = integer(a[2], "E");
         if (E < 1) throw Refused("E must be positive");
         const int64_t pairs = (int64_t)T * k;
         const auto* ip = at_of<int32_t>(&idx, "idx", at::kInt, {T, k}, dev);
@@ -213,6 +227,7 @@ PyObject* dispatch_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
         check(moe_dispatch_rows(xp, dt, T, H, ip, k, E, rp, offsets.data_ptr<int32_t>(), perm.data_ptr<int32_t>(),
                                 pos.data_ptr<int32_t>(), need ? ws.data_ptr() : nullptr, need, stream_of(dev)));
         written({into});
+        unlocked.end();
         return pack(rows, offsets, perm, pos);
     });
 }
@@ -223,6 +238,7 @@ PyObject* dispatch_rows_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         expect_args(n, 3, "dispatch_rows_backward");
         const Tensor &drows = tensor(a[0], "drows"), &pos = tensor(a[1], "pos");
         const Tensor* into = optional_tensor(a[2], "out");
+        Unlocked unlocked;
         const int dev = device_of(drows, "drows");
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
         const auto [R, H] = matrix(drows, "drows");
@@ -235,6 +251,7 @@ PyObject* dispatch_rows_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         void* op = at_of(&out, "out", st, {T, H}, dev);
         check(moe_dispatch_rows_backward(dp, dt, R, pp, T, k, H, op, stream_of(dev)));
         written({into});
+        unlocked.end();
         return wrap(out);
     });
 }
@@ -245,6 +262,7 @@ PyObject* combine_weighted(PyObject*, PyObject* const* a, Py_ssize_t n) {
         expect_args(n, 5, "combine_weighted");
         const Tensor &rows = tensor(a[0], "rows"), &pos = tensor(a[1], "pos"), &gates = tensor(a[2], "gates");
         const Tensor *base = optional_tensor(a[3], "base"), *into = optional_tensor(a[4], "out");
+        Unlocked unlocked;
         const int dev = device_of(rows, "rows");
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
         const auto [R, H] = matrix(rows, "rows");
@@ -259,6 +277,7 @@ PyObject* combine_weighted(PyObject*, PyObject* const* a, Py_ssize_t n) {
         void* op = at_of(&out, "out", st, {T, H}, dev);
         check(moe_combine_weighted(rp, dt, R, pp, gp, T, k, H, bp, op, stream_of(dev)));
         written({into});
+        unlocked.end();
         return wrap(out);
     });
 }
@@ -270,6 +289,7 @@ PyObject* combine_weighted_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
         const Tensor &dout = tensor(a[0], "dout"), &rows = tensor(a[1], "rows"), &pos = tensor(a[2], "pos"),
                      &gates = tensor(a[3], "gates");
         const Tensor* into = optional_tensor(a[4], "drows");
+        Unlocked unlocked;
         const int dev = device_of(rows, "rows");
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
         const auto [R, H] = matrix(rows, "rows");
@@ -284,6 +304,7 @@ PyObject* combine_weighted_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
         void* dp = at_of(&drows, "drows", st, {R, H}, dev);
         check(moe_combine_weighted_backward(op, dt, rp, R, pp, gp, T, k, H, dp, dgates.data_ptr<float>(), stream_of(dev)));
         written({into});
+        unlocked.end();
         return pack(drows, dgates);
     });
 }
@@ -301,6 +322,7 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const float scale = real(a[5], "scale"), eps = real(a[6], "eps");
         const bool norm_post = truth(a[7], "norm_post"), pre = truth(a[11], "pre");
         const int given = integer(a[8], "n_dtype");
+        Unlocked unlocked;
         const int dev = device_of(h, "h");
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
         const auto [T, H] = matrix(h, "h");
@@ -323,6 +345,7 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
                              norm_post ? r_post.data_ptr<float>() : nullptr, pre ? r_pre.data_ptr<float>() : nullptr,
                              stream_of(dev)));
         written({h_into, n_into});
+        unlocked.end();
         return pack(h_out, n_out, r_post, r_pre);
     });
 }
@@ -338,6 +361,7 @@ PyObject* block_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
                      *w_pre = optional_tensor(a[6], "w_pre"), *w_post = optional_tensor(a[7], "w_post"),
                      *gate = optional_tensor(a[8], "gate");
         const float scale = real(a[9], "scale");
+        Unlocked unlocked;
         const int dev = device_of(h, "h_out");
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
         const auto [T, H] = matrix(h, "h_out");
@@ -359,6 +383,7 @@ PyObject* block_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         check(moe_block_norm_backward(np, ip, hp, hd, yp, yd, T, H, rp, rq, wp, wq, r_post != nullptr, gp, scale, ptr(dh), ptr(dy),
                                       static_cast<float*>(ptr(dw_pre)), static_cast<float*>(ptr(dw_post)),
                                       static_cast<float*>(ptr(dgate)), ptr(ws), need, stream_of(dev)));
+        unlocked.end();
         return pack(dh, dy, dw_pre, dw_post, dgate);
     });
 }
@@ -371,6 +396,7 @@ PyObject* mx4_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Tensor& x = tensor(a[0], "x");
         const Tensor *pos = optional_tensor(a[1], "pos"), *c_into = optional_tensor(a[3], "codes"), *s_into = optional_tensor(a[4], "scales");
         const int act = integer(a[2], "act");
+        Unlocked unlocked;
         const int dev = device_of(x, "x");
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
         const auto [T, W] = matrix(x, "x");
@@ -388,6 +414,7 @@ PyObject* mx4_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
         auto* sp = at_of<uint8_t>(&scales, "scales", at::kByte, {rows, K / 32}, dev);
         check(moe_mx4_quantize(xp, dt, T, K, act, pp, k, rows, cp, sp, stream_of(dev)));
         written({c_into, s_into});
+        unlocked.end();
         return pack(codes, scales);
     });
 }
@@ -398,6 +425,7 @@ PyObject* mx4_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
         expect_args(n, 3, "mx4_dequantize");
         const Tensor &codes = tensor(a[0], "codes"), &scales = tensor(a[1], "scales");
         const int dt = integer(a[2], "dtype");
+        Unlocked unlocked;
         const int dev = device_of(codes, "codes");
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
         if (codes.dim() < 1) throw Refused("codes: a tensor of rows is needed");
@@ -409,6 +437,7 @@ PyObject* mx4_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
         shape.back() = K;
         Tensor out = empty(shape, scalar_type(dt), dev);
         check(moe_mx4_dequantize(cp, sp, K ? out.numel() / K : 0, K, out.data_ptr(), dt, stream_of(dev)));
+        unlocked.end();
         return wrap(out);
     });
 }
@@ -421,6 +450,7 @@ PyObject* mx4_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
                      &w_scales = tensor(a[3], "w_scales"), &offsets = tensor(a[4], "offsets");
         const Tensor* into = optional_tensor(a[5], "out");
         const int dt = integer(a[6], "dtype");
+        Unlocked unlocked;
         const int dev = device_of(codes, "codes");
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
         const auto [R, Kh] = matrix(codes, "codes");
@@ -435,6 +465,7 @@ PyObject* mx4_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
         void* op = at_of(&out, "out", out.scalar_type(), {R, N}, dev);
         check(moe_mx4_matmul(cp, sp, R, K, wp, wq, E, N, fp, op, rows_dtype(out.scalar_type(), "out"), stream_of(dev)));
         written({into});
+        unlocked.end();
         return wrap(out);
     });
 }

@@ -5,6 +5,7 @@ import os
 import subprocess
 import sys
 import threading
+import time
 
 import pytest
 import torch
@@ -814,3 +815,57 @@ def test_norm_gradients_of_two_widths_from_two_threads():
     if errors:
         raise errors[0]
     assert got == [calls, calls] and ops.status() == M.MOE_OK
+
+
+def test_a_call_that_waits_leaves_other_threads_running():
+    """A stream about a second behind fills its launch queue: the next call waits for room, and Python's other threads must
+    not wait with it."""
+    codes, scales = torch.zeros((32, 64), dtype=torch.uint8, device="cuda"), torch.zeros((32, 4), dtype=torch.uint8, device="cuda")
+    ops.mx4_dequantize(codes, scales)
+    torch.cuda.synchronize()
+    gaps, stop = [0.0], threading.Event()
+
+    def tick():
+        last = time.perf_counter()
+        while not stop.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            gaps.append(now - last)
+            last = now
+
+    other = threading.Thread(target=tick)
+    other.start()
+    try:
+        behind = torch.cuda.Event()
+        torch.cuda._sleep(int(2e9))
+        behind.record()
+        start = time.perf_counter()
+        while not behind.query():
+            ops.mx4_dequantize(codes, scales)
+        took = time.perf_counter() - start
+    finally:
+        stop.set()
+        other.join()
+    torch.cuda.synchronize()
+    assert max(gaps) < took / 2, f"another thread waited {max(gaps):.3f} of {took:.3f} s"
+    assert ops.status() == M.MOE_OK
+
+
+def test_refusals_from_many_threads():
+    """Errors are raised with the interpreter's lock held again, whatever step found them."""
+    x, idx = torch.zeros((4, 64), device="cuda"), torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    raised = []
+
+    def refuse():
+        for _ in range(200):
+            for call, error in ((lambda: ops.dispatch_rows(x[:3], idx, 4), ValueError), (lambda: ops.dispatch_rows(x, idx, 257), M.MoeError),
+                                (lambda: ops.block_norm(x, eps=-1.0), M.MoeError), (lambda: ops.mx4_quantize(x.cpu()), ValueError)):
+                try:
+                    call()
+                except error as e:
+                    raised.append(str(e))
+
+    threads = [threading.Thread(target=refuse) for _ in range(4)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert len(raised) == 4 * 200 * 4 and ops.status() == M.MOE_OK
