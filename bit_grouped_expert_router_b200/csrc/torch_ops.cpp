@@ -6,6 +6,7 @@
 // passing a dozen arguments from Python took 8 to 12 us more.  Functions take their arguments by
 // position (None for an absent tensor), run on the tensors' device and its current stream, and return
 // the outputs; a tensor the library cannot take raises ValueError, a refusal by the library MoeError.
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
@@ -52,8 +53,8 @@ template <typename F> PyObject* guarded(F f) {
             PyErr_SetObject(g_moe_error, err);
             Py_DECREF(err);
         }
-    } catch (const std::exception& e) {   // an allocation that failed, say
-        if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (const std::exception&) {   // torch's own: memory that ran out raises the class that programs catch for it
+        if (!PyErr_Occurred()) torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }

@@ -7,7 +7,8 @@ Argument marshalling only, like ``_lib`` (the tensors are checked and passed on 
 ``_torch_ops``); every step runs in the CUDA library.  The functions take dense, contiguous CUDA tensors of
 one device, run there on ``stream`` (default: that device's current stream) without synchronising, and allocate
 what they return, and their scratch, on that stream unless an output tensor is given.  A wrong tensor raises
-ValueError, a refusal by the library MoeError; what the kernels find on the device is kept for ``status``.
+ValueError, a refusal by the library MoeError, memory that runs out torch.OutOfMemoryError; what the kernels find on the
+device is kept for ``status``.
 Tensors passed with ``stream`` must be ready there and stay alive until the stream has passed the call.  No graph of
 automatic differentiation is recorded, not even for tensors that require gradients: the gradients are functions of their
 own.  A tensor given to be written counts as modified in place, so a graph that had saved its values refuses to use them.

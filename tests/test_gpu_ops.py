@@ -869,3 +869,18 @@ def test_refusals_from_many_threads():
     [t.start() for t in threads]
     [t.join() for t in threads]
     assert len(raised) == 4 * 200 * 4 and ops.status() == M.MOE_OK
+
+
+def test_an_allocation_that_fails_raises_torchs_error():
+    codes = torch.zeros((1 << 15, 2048), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((1 << 15, 128), dtype=torch.uint8, device="cuda")
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (64 << 20)) / total)
+    try:
+        with pytest.raises(torch.OutOfMemoryError, match="out of memory"):     # 512 MiB of values
+            ops.mx4_dequantize(codes, scales, dtype=torch.float32)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert ops.mx4_dequantize(codes, scales, dtype=torch.float32).shape == (1 << 15, 4096)
+    assert ops.status() == M.MOE_OK
