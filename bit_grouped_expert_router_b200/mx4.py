@@ -43,9 +43,9 @@ class Mx4Experts:
     def forward(self, x, idx, gates, base=None, out=None, *, stream=None):
         """out [T, H] = base + sum_j gates[:, j] * FFN_{idx[:, j]}(x) for x [T, H] bf16, idx [T, k] int32 (negative: none)
         and gates [T, k] fp32."""
-        if stream is not None:
-            with torch.cuda.stream(stream):
-                return self.forward(x, idx, gates, base, out)
+        return ops._run(self._forward, stream, x, idx, gates, base, out)
+
+    def _forward(self, x, idx, gates, base, out):
         d = ops.dispatch_rows(None, idx, self.E)
         codes, scales = ops.mx4_quantize(x, pos=d.pos)
         h = ops.mx4_matmul(codes, scales, *self.gateup, d.offsets)

@@ -163,3 +163,16 @@ def test_plain_norm_gradient_is_the_difference_quotient():
             down.view(-1)[at] -= 1e-5
             # central differences: 1e-10 of a third derivative, and 1e-16 / 1e-5 of the loss
             assert abs((loss(**{name: up}) - loss(**{name: down})) / 2e-5 - float(grad[of][0].reshape(-1)[at])) < 1e-6
+
+
+def test_experts_refuse_a_stream_of_another_device(lib):
+    """As each operator does: the steps would run on the tensors' device, on a stream that nobody waits for."""
+    from types import SimpleNamespace
+
+    from bit_grouped_expert_router_b200.mx4 import Mx4Experts
+    packed = lambda n, k: (torch.zeros((2, n, k // 2), dtype=torch.uint8), torch.zeros((2, n, k // 32), dtype=torch.uint8))  # noqa: E731
+    ex = Mx4Experts(packed(64, 64), packed(64, 32))
+    x, idx, gates = torch.zeros((3, 64)), torch.zeros((3, 1), dtype=torch.int32), torch.zeros((3, 1))
+    other = SimpleNamespace(device=torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="the stream is of cuda:1, a tensor of cpu"):
+        ex.forward(x, idx, gates, stream=other)
