@@ -5,7 +5,9 @@ the CUDA runtime linked statically, so loading the library needs no GPU driver (
 inspected on a machine without a GPU; the first CUDA call needs one).
 
 _torch_ops.so is the Python module behind ops.py (csrc/torch_ops.cpp: torch tensors in, libmoe calls out);
-it compiles against the installed torch and links to the libmoe.so next to it.
+it compiles against the installed torch and links to the libmoe.so next to it.  The library stands without it: where
+there is no torch the module is left out, and where it does not compile a warning says why (ops.py then fails at its first
+call).
 """
 from __future__ import annotations
 
@@ -13,6 +15,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -35,18 +38,32 @@ def _nvcc() -> str:
     return "nvcc"
 
 
-def _deps():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "moe.h"))
-    files.append(os.path.abspath(__file__))
-    return files
+EXT_SOURCE = "torch_ops.cpp"
+
+
+def _newer(target: str, sources) -> bool:
+    files = [os.path.join(CSRC, f) for f in sources] + [os.path.join(INCLUDE, "moe.h"), os.path.abspath(__file__)]
+    return os.path.exists(target) and all(os.path.getmtime(f) <= os.path.getmtime(target) for f in files)
+
+
+def _has_torch() -> bool:
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return False
+    return True
+
+
+def _lib_up_to_date() -> bool:
+    return _newer(LIB, [f for f in os.listdir(CSRC) if f != EXT_SOURCE])
+
+
+def _ext_up_to_date() -> bool:
+    return not _has_torch() or _newer(EXT, [EXT_SOURCE])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(EXT):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    return _lib_up_to_date() and _ext_up_to_date()
 
 
 # The decode GEMVs feed 4-bit codes to fp32 FMAs as IEEE subnormals (code * 2^-149, see
@@ -74,10 +91,10 @@ def _compile_ext(obj: str) -> None:
     cmd = [HOST_CXX, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", sysconfig.get_paths()["include"],
            "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
-           "-c", os.path.join(CSRC, "torch_ops.cpp"), "-o", obj]
+           "-c", os.path.join(CSRC, EXT_SOURCE), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"torch_ops.cpp failed:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"{EXT_SOURCE} failed:\n{r.stdout}\n{r.stderr}")
 
 
 def _link_ext(obj: str) -> None:
@@ -94,7 +111,8 @@ def _link_ext(obj: str) -> None:
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     check_flags(list(NVCC_FLAGS) + list(extra_flags))
-    if not force and up_to_date():
+    want_lib, want_ext = force or not _lib_up_to_date(), _has_torch() if force else not _ext_up_to_date()
+    if not want_lib and not want_ext:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -111,19 +129,26 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stderr, file=sys.stderr)
         return obj
 
-    ext_obj = os.path.join(BUILD, "torch_ops.cpp.o")
+    ext_obj = os.path.join(BUILD, EXT_SOURCE + ".o")
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        ext = ex.submit(_compile_ext, ext_obj)
-        objs = list(ex.map(compile_one, SOURCES))
-        ext.result()
-    tmp = LIB + ".tmp"
-    cmd = [nvcc, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-cudart", "static",
-           "-Xcompiler", "-fPIC", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    _link_ext(ext_obj)
+        ext = ex.submit(_compile_ext, ext_obj) if want_ext else None
+        if want_lib:
+            objs = list(ex.map(compile_one, SOURCES))
+            tmp = LIB + ".tmp"
+            cmd = [nvcc, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-cudart", "static",
+                   "-Xcompiler", "-fPIC", "-o", tmp, *objs]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+            os.replace(tmp, LIB)
+    if ext:
+        try:
+            ext.result()
+            _link_ext(ext_obj)
+        except RuntimeError as e:
+            if os.path.exists(EXT):
+                os.remove(EXT)   # of an older source: it must not pass for this one's
+            warnings.warn(f"libmoe is built, _torch_ops is not: {e}", RuntimeWarning, stacklevel=2)
     return LIB
 
 

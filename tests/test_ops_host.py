@@ -1,6 +1,9 @@
 """Host-side checks of the operators around the experts (no GPU needed): each entry point refuses bad
 arguments before it touches the device, and the Python calls refuse tensors they cannot pass on."""
+import ctypes
 import inspect
+import os
+import sys
 
 import pytest
 import torch
@@ -176,3 +179,37 @@ def test_experts_refuse_a_stream_of_another_device(lib):
     other = SimpleNamespace(device=torch.device("cuda", 1))
     with pytest.raises(ValueError, match="the stream is of cuda:1, a tensor of cpu"):
         ex.forward(x, idx, gates, stream=other)
+
+
+@pytest.fixture
+def small_tree(tmp_path, monkeypatch):
+    """The build pointed at a tree of one small source."""
+    src = tmp_path / "csrc"
+    src.mkdir()
+    (src / "one.cu").write_text('extern "C" __attribute__((visibility("default"))) int one() { return 1; }\n')
+    (src / "torch_ops.cpp").write_text("#error this module does not compile\n")
+    for name, value in dict(CSRC=str(src), BUILD=str(tmp_path / "obj"), LIB=str(tmp_path / "libmoe.so"), SOURCES=["one.cu"],
+                            PKG=str(tmp_path), EXT=str(tmp_path / os.path.basename(B.EXT))).items():
+        monkeypatch.setattr(B, name, value)
+    return tmp_path
+
+
+def test_the_library_is_built_where_its_torch_module_does_not_compile(small_tree):
+    """The C ABI needs nvcc only; the module's failure is told all the same, and again on the next call, and a module of an
+    older source does not stay behind."""
+    for _ in range(2):
+        with open(B.EXT, "w"):
+            os.utime(B.EXT, (0, 0))
+        with pytest.warns(RuntimeWarning, match="torch_ops.cpp failed"):
+            assert B.build() == B.LIB
+        assert ctypes.CDLL(B.LIB).one() == 1
+        assert not B.up_to_date() and not os.path.exists(B.EXT)
+
+
+def test_the_library_is_built_without_torch(small_tree, monkeypatch):
+    monkeypatch.setitem(sys.modules, "torch", None)      # import torch raises ImportError
+    assert B.build() == B.LIB
+    assert ctypes.CDLL(B.LIB).one() == 1
+    made = os.stat(B.LIB).st_mtime_ns
+    B.build()
+    assert os.stat(B.LIB).st_mtime_ns == made            # nothing left to build
