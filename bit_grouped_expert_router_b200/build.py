@@ -1,11 +1,12 @@
-"""In-tree build of libmoe.so (the CUDA library behind include/moe.h) for sm_100a, and of _torch_ops.so.
+"""In-tree build of libmoe.so (the CUDA library behind include/moe.h) for sm_100a, and of its torch module.
 
 Each .cu file compiles to an object in parallel; the objects link into one shared library with
 the CUDA runtime linked statically, so loading the library needs no GPU driver (symbols can be
 inspected on a machine without a GPU; the first CUDA call needs one).
 
-_torch_ops.so is the Python module behind ops.py (csrc/torch_ops.cpp: torch tensors in, libmoe calls out);
-it compiles against the installed torch and links to the libmoe.so next to it.  The library stands without it: where
+_torch_ops is the Python module behind ops.py (csrc/torch_ops.cpp: torch tensors in, libmoe calls out);
+it compiles against the installed torch and links to the libmoe.so next to it.  Its file's name has Python's tag, and it
+holds the version of torch, so another Python or torch gets one of its own.  The library stands without it: where
 there is no torch the module is left out, and where it does not compile a warning says why (ops.py then fails at its first
 call).
 """
@@ -24,7 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
-EXT = os.path.join(PKG, "_torch_ops.so")
+EXT = os.path.join(PKG, "_torch_ops" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["api.cu", "repack.cu", "route.cu", "router_tc.cu", "gemm.cu", "decode.cu", "decode_fused.cu", "route_static.cu",
            "ops_api.cu", "rows.cu", "norm.cu", "mx4.cu"]
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
@@ -58,8 +59,19 @@ def _lib_up_to_date() -> bool:
     return _newer(LIB, [f for f in os.listdir(CSRC) if f != EXT_SOURCE])
 
 
+def built_for() -> str:
+    """What the module is compiled against, as it says itself (``_torch_ops.built_for``)."""
+    import torch
+    return f"torch {torch.__version__}"
+
+
 def _ext_up_to_date() -> bool:
-    return not _has_torch() or _newer(EXT, [EXT_SOURCE])
+    if not _has_torch():
+        return True
+    if not _newer(EXT, [EXT_SOURCE]):
+        return False
+    with open(EXT, "rb") as f:
+        return built_for().encode() + b"\0" in f.read()
 
 
 def up_to_date() -> bool:
@@ -88,7 +100,7 @@ def _compile_ext(obj: str) -> None:
     import torch
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
-    cmd = [HOST_CXX, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+    cmd = [HOST_CXX, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f'-DMOE_BUILT_FOR="{built_for()}"',
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", sysconfig.get_paths()["include"],
            "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
            "-c", os.path.join(CSRC, EXT_SOURCE), "-o", obj]
@@ -101,6 +113,9 @@ def _link_ext(obj: str) -> None:
     import torch
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = EXT + ".tmp"
+    old = os.path.join(PKG, "_torch_ops.so")   # an earlier build's, without the tag: any Python would find it
+    if os.path.exists(old):
+        os.remove(old)
     cmd = [HOST_CXX, "-shared", obj, "-o", tmp, "-L", PKG, "-l:libmoe.so", "-L", lib, "-ltorch_python",
            "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)

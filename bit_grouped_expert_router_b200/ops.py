@@ -21,6 +21,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _lib as M
+from .build import built_for
 
 _DTYPES = {torch.bfloat16: M.MOE_DTYPE_BF16, torch.float16: M.MOE_DTYPE_FP16, torch.float32: M.MOE_DTYPE_FP32}
 _ACTS = {None: M.MOE_ACT_NONE, "swiglu": M.MOE_ACT_SWIGLU}
@@ -61,6 +62,9 @@ def _ext():
         except ImportError as e:
             raise ImportError(f"_torch_ops is not built or does not load ({e}); "
                               "run bit_grouped_expert_router_b200.build.build()") from e
+        if _torch_ops.built_for != built_for():
+            raise ImportError(f"_torch_ops was built for {_torch_ops.built_for}, this is {built_for()}; "
+                              "run bit_grouped_expert_router_b200.build.build()")
         _torch_ops.set_error(M.MoeError)
         _x = _torch_ops
     return _x

@@ -4,6 +4,7 @@ import ctypes
 import inspect
 import os
 import sys
+import sysconfig
 
 import pytest
 import torch
@@ -213,3 +214,16 @@ def test_the_library_is_built_without_torch(small_tree, monkeypatch):
     made = os.stat(B.LIB).st_mtime_ns
     B.build()
     assert os.stat(B.LIB).st_mtime_ns == made            # nothing left to build
+
+
+def test_a_module_of_another_torch_or_python_is_not_taken(lib, monkeypatch):
+    """Its classes and calls are those of the torch and the Python it was compiled against."""
+    assert B.EXT.endswith(sysconfig.get_config_var("EXT_SUFFIX"))      # another Python does not find it
+    assert B.up_to_date()
+    monkeypatch.setattr(ops, "_x", None)
+    assert ops._ext().built_for == f"torch {torch.__version__}"
+    monkeypatch.setattr(torch, "__version__", "1.0.0+other")
+    assert not B.up_to_date()
+    monkeypatch.setattr(ops, "_x", None)
+    with pytest.raises(ImportError, match="1.0.0.other"):
+        ops._ext()
