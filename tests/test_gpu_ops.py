@@ -884,3 +884,48 @@ def test_an_allocation_that_fails_raises_torchs_error():
         torch.cuda.set_per_process_memory_fraction(1.0)
     assert ops.mx4_dequantize(codes, scales, dtype=torch.float32).shape == (1 << 15, 4096)
     assert ops.status() == M.MOE_OK
+
+
+def test_an_error_is_told_once_and_both_callers_come_to_their_end():
+    """As above, with what each caller met: an exception in one of them, or a call left out, is a failure."""
+    idx = torch.full((1, 1), 9, dtype=torch.int32, device="cuda")   # no expert of four
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    start, calls = threading.Barrier(2, timeout=60), 100
+    got, errors = [[], []], []
+
+    def take(i):
+        try:
+            for _ in range(calls):
+                start.wait()
+                if i == 0:
+                    ops.dispatch_rows(None, idx, 4)
+                    torch.cuda.current_stream().synchronize()
+                start.wait()
+                got[i].append(ops.status(streams[i]))
+        except BaseException as e:
+            errors.append(e)
+            start.abort()
+
+    threads = [threading.Thread(target=take, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    if errors:
+        raise errors[0]
+    assert len(got[0]) == len(got[1]) == calls
+    assert all(sorted(pair) == sorted((M.MOE_OK, M.MOE_ERR_DEVICE_BOUNDS)) for pair in zip(*got))
+
+
+@pytest.mark.parametrize("w_scale", [1, 27, 127, 200, 254])
+def test_matmul_of_scales_far_from_one_another(w_scale):
+    """Scales at the ends of their range whose product is an ordinary number, or ends above or below fp32."""
+    N, K = 128, 64
+    x = torch.arange(0, 255, 2)
+    scales = x.to(torch.uint8).view(-1, 1).repeat(1, K // 32)
+    codes = torch.full((len(x), K // 2), 0x22, dtype=torch.uint8)          # ones
+    w, ws = torch.full((1, N, K // 2), 0x22, dtype=torch.uint8), torch.full((1, N, K // 32), w_scale, dtype=torch.uint8)
+    offsets = torch.tensor([0, len(x)], dtype=torch.int32)
+    got = ops.mx4_matmul(*[t.cuda() for t in (codes, scales, w, ws, offsets)], dtype=torch.float32).cpu()
+    want = (64.0 * torch.exp2((x + w_scale - 254).double())).float().view(-1, 1).expand(-1, N)
+    normal = want >= torch.finfo(torch.float32).smallest_normal
+    assert torch.equal(got[normal], want[normal])
+    assert (got[~normal] <= torch.finfo(torch.float32).smallest_normal).all() and (got >= 0).all()
