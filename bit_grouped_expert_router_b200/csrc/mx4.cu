@@ -105,6 +105,7 @@ __device__ __forceinline__ float max_magnitude(float a, float b) {
 // written (4096 and 16384 tokens of 2048 to 8 rows each: 10.7 and 35.9 us with one item, 11.8 and 39.7 with two;
 // 131072 x 512 in order: 26.0 and 25.7 us).
 __host__ __device__ constexpr int quant_items(bool pos) { return pos ? 1 : 2; }
+
 // The loaded items quantised and stored.
 template <typename T, bool SWIGLU, bool POS, bool TAIL>
 __device__ __forceinline__ void quantize_items(const Mx4QuantArgs& a, uint32_t items, uint32_t i0,
@@ -255,11 +256,11 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t* __r
 // 2 x 32 columns of scales, alternating by step.
 //
 // What bounds it: the weights from HBM while the rows are few (1024 rows over 256 experts of 1024 x 2048: 47.7 us of
-// 43.0), then the traffic from L2 (weights once per row tile, rows once per feature tile: 699 MB of it
-// in the 73 us of 32768 x 1024 x 2048 over 256 experts), and, run after run, the power cap (1.65 GHz and 87 us
-// there).  Short rows and many results (32768 x 2048 x 512: 62 us of 43.6, in fp32 104 of 64.1) leave DRAM and L2 about
-// half busy; what holds them is not known.  Pairs of CTAs on one tile of 256 features (cta_group::2), which read the rows half as often, gained
-// 3 to 5% from 131072 rows on and lost 1 to 30% below: their barriers and commits cross CTAs every step.
+// 43.0), then the traffic from L2 (weights once per row tile, rows once per feature tile: 699 MB of it in the 73 us of
+// 32768 x 1024 x 2048 over 256 experts), and, run after run, the power cap (1.65 GHz and 87 us there).  Short rows and
+// many results (32768 x 2048 x 512: 62 us of 43.6, in fp32 104 of 64.1) leave DRAM and L2 about half busy; what holds
+// them is not known.  Pairs of CTAs on one tile of 256 features (cta_group::2), which read the rows half as often,
+// gained 3 to 5% from 131072 rows on and lost 1 to 30% below: their barriers and commits cross CTAs every step.
 constexpr int kTM = 128;             // features per unit
 constexpr int kStep = 256;           // columns per step: 128 bytes of codes per row
 constexpr int kSfSteps = 4;          // steps whose scales come together: a 32-byte sector of every row

@@ -303,9 +303,9 @@ MOE_API int moe_route_static(const uint16_t *x, int32_t T, int32_t H, const floa
  *  - No handle: the calls run on the CURRENT device (all pointers belong to it) and on `stream`, own
  *    no memory and keep nothing between calls.  Whatever scratch a call needs is the caller's
  *    `workspace` (16-byte aligned, at least the size the matching *_workspace function gives; it need
- *    not be cleared and holds nothing afterwards).  Calls may be made from several threads at a time, may overlap on
- *    the device as long as their buffers do not, and may be captured in CUDA graphs; replays of graphs that share a workspace or
- *    an output must not overlap.
+ *    not be cleared and holds nothing afterwards).  Calls may be made from several threads at a time and
+ *    may overlap on the device as long as their buffers do not, and may be captured in CUDA graphs;
+ *    replays of graphs that share a workspace or an output must not overlap.
  *  - Rows are densely packed, of H values with H % 8 == 0, in one of the MOE_DTYPE_* types; sums,
  *    row factors, gates and norm weights are fp32; each result is rounded once, to nearest (ties to
  *    even).  No sum uses atomics: equal inputs give equal bits.
@@ -375,9 +375,10 @@ MOE_API int moe_block_norm(const void *h, int32_t h_dtype, const void *y, int32_
 
 /* Its gradient, from dn[T, H] (the gradient of n_out, y_dtype; NULL: none) and dh_out[T, H] (that of h_out, h_dtype;
  * NULL: none), with h_out, r_pre (needed with dn) and r_post (needed with norm_post) as the forward
- * call left them.  (That call took n and r_pre from h' before its rounding; here z = h_out * r_pre stands for the
- * normed row, so for a 16-bit h_out the gradient is that of a point half a rounding step away.)  Results, each NULL to skip it: dh[T, H] (h_dtype), dy[T, H] (y_dtype), dw_pre[H],
- * dw_post[H], dgate[T] (fp32; dw_pre needs dn; dy, dw_post and dgate need y).  dh may be dh_out, dy may be dn. */
+ * call left them.  (That call took n and r_pre from h' before its rounding; here h_out * r_pre stands for
+ * the normed row, so for a 16-bit h_out the gradient is that of a point half a rounding step away.)
+ * Results, each NULL to skip it: dh[T, H] (h_dtype), dy[T, H] (y_dtype), dw_pre[H], dw_post[H], dgate[T]
+ * (fp32; dw_pre needs dn; dy, dw_post and dgate need y).  dh may be dh_out, dy may be dn. */
 MOE_API size_t moe_block_norm_backward_workspace(int32_t T, int32_t H);
 MOE_API int moe_block_norm_backward(const void *dn, const void *dh_out, const void *h_out, int32_t h_dtype,
                                     const void *y, int32_t y_dtype, int32_t T, int32_t H, const float *r_pre,
